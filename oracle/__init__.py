@@ -28,6 +28,13 @@ Modules:
              its written specification and hand-made fixtures only
   attention  decode attention on the packed cache, two ways        -- pinned
   opcount    instrumented op counter for the rotation              -- pinned
+  cache8     the 8-bit cache: block scales, appends, attention     -- pinned (torch's
+             float8 conversion, torch SDPA in fp64)
+  rope       rotary frequencies and rotation of pairs              -- pinned (rotation
+             matrices, closed forms)
+  pages      the block table's operations on Python lists          -- pinned by hand-worked
+             examples
 """
 
 from . import codebook, rotation, encode, packing, attention, opcount  # noqa: F401
+from . import cache8, pages, rope  # noqa: F401,E402

@@ -22,16 +22,29 @@ IQ_ERR_ALIGNMENT = 5
 IQ_ERR_CUDA = 6
 IQ_F16 = 0
 IQ_F32 = 1
+IQ_BF16 = 2  # the calls on the 8-bit cache and iq_rope only
 IQ_DEVERR_POSITION = 1
 IQ_DEVERR_PAGE = 2
 IQ_DEVERR_CTX = 4
 IQ_DEVERR_TIMEOUT = 8
 IQ_DEVERR_WORKSPACE = 16
+IQ_DEVERR_SEQ = 32
+IQ_DEVERR_NOPAGE = 64
 IQ_ROT_ISO = 0
 IQ_ROT_QUAT = 1
 IQ_ROT_PLANAR = 2
 ROTATIONS = {"iso": IQ_ROT_ISO, "quat": IQ_ROT_QUAT, "planar": IQ_ROT_PLANAR}
 WIDTHS = ((2, 2), (3, 2), (3, 3), (4, 2), (4, 3), (4, 4))  # supported (K bits, V bits)
+
+IQ_E4M3 = 0
+IQ_S8 = 1
+CODES8 = {"e4m3": IQ_E4M3, "s8": IQ_S8}
+TILE8_BYTES = 8224
+IQ_ROPE_HALF = 0
+IQ_ROPE_INTERLEAVED = 1
+ROPE_LAYOUTS = {"half": IQ_ROPE_HALF, "interleaved": IQ_ROPE_INTERLEAVED}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+IQ_PAGES_MAX_LIST = 4096
 
 HEAD_DIM = 128
 V_BLOCK_TOKENS = 16
@@ -88,6 +101,43 @@ class iq_fp16_prefix(ctypes.Structure):
     ]
 
 
+class iq_cache8(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("n_layers", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("block_table_dev", ctypes.c_void_p),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("status_dev", ctypes.c_void_p),
+        ("code", ctypes.c_int32),
+    ]
+
+
+class iq_pages(ctypes.Structure):
+    _fields_ = [
+        ("block_table_dev", ctypes.c_void_p),
+        ("seq_len_dev", ctypes.c_void_p),
+        ("ref_dev", ctypes.c_void_p),
+        ("max_seqs", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("status_dev", ctypes.c_void_p),
+    ]
+
+
+class iq_page_pool(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("n_layers", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("tile_bytes", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 
@@ -133,6 +183,29 @@ def lib():
         L.iq_prefill_attention.argtypes = [P, i32, vp, ctypes.c_int, i32, i32, i32, vp, i32, vp, vp, vp, sz, vp]
         L.iq_export_codes.restype = ctypes.c_int
         L.iq_export_codes.argtypes = [P, i32, i32, i32, i32, i32, vp, vp, vp]
+        f32, f64, i64 = ctypes.c_float, ctypes.c_double, ctypes.c_int64
+        P8, PG, PP = ctypes.POINTER(iq_cache8), ctypes.POINTER(iq_pages), ctypes.POINTER(iq_page_pool)
+        for name, res, args in (
+            ("iq_cache8_bytes", ctypes.c_int, [i32, i32, i32, i32, ctypes.POINTER(sz)]),
+            ("iq_append8", ctypes.c_int, [P8, i32, vp, vp, ctypes.c_int, i64, i64, i32, i32, vp, vp, vp]),
+            ("iq_decode8_workspace_size", sz, [i32, i32, i32, i32]),
+            ("iq_decode8_attention", ctypes.c_int, [P8, i32, vp, ctypes.c_int, i32, i32, vp, i32, f32, vp, vp, sz, vp]),
+            ("iq_prefill8_workspace_size", sz, [i32, i32, i32, i32, i32]),
+            ("iq_prefill8_attention", ctypes.c_int, [P8, i32, vp, ctypes.c_int, i32, i32, i32, vp, vp, i32, f32, vp, vp,
+                                                     sz, vp]),
+            ("iq_export8", ctypes.c_int, [P8, i32, i32, i32, i32, i32, vp, vp]),
+            ("iq_rope_frequencies", ctypes.c_int, [i32, f64, i32, f64, f64, f64, f64, vp, ctypes.POINTER(f64)]),
+            ("iq_rope", ctypes.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, i32, i32, i32, i32, i32, vp, vp,
+                                       f32, i32, vp]),
+            ("iq_pages_workspace_size", sz, [PG]),
+            ("iq_pages_extend", ctypes.c_int, [PG, vp, vp, i32, vp, sz, vp]),
+            ("iq_pages_free", ctypes.c_int, [PG, vp, i32, vp]),
+            ("iq_pages_fork", ctypes.c_int, [PG, PP, i32, vp, vp, i32, vp, sz, vp]),
+            ("iq_pages_compact", ctypes.c_int, [PG, PP, i32, vp, vp, sz, vp]),
+            ("iq_pages_copy", ctypes.c_int, [PG, PP, i32, vp, vp, i32, vp, sz, vp]),
+        ):
+            getattr(L, name).restype = res
+            getattr(L, name).argtypes = args
         _lib = L
     return _lib
 
@@ -340,3 +413,341 @@ class PagedCache:
 
     def v_norm_view(self):
         return self.v_norms
+
+
+# ----------------------------------------------------------------------- the 8-bit cache, rotary positions, pages
+# These calls run on the device of their tensors, whichever is current, and on that device's current
+# stream unless one is given.  A tensor of the wrong shape, type, layout or device is a ValueError.
+def _bad(fn, what):
+    raise ValueError(f"{fn}: {what}")
+
+
+def _dtype(fn, t):
+    import torch
+
+    if t.dtype == torch.float16:
+        return IQ_F16
+    if t.dtype == torch.bfloat16:
+        return IQ_BF16
+    if t.dtype == torch.float32:
+        return IQ_F32
+    _bad(fn, f"float16, bfloat16 or float32 wanted, got {t.dtype}")
+
+
+def _plain(fn, name, t, dev, dtype, shape):
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(fn, f"{name}: a contiguous {dtype} tensor of shape {shape} on cuda:{dev} wanted, got {t.dtype} "
+                 f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+def _i32(fn, name, t, dev, n):
+    import torch
+
+    return _plain(fn, name, t, dev, torch.int32, (n,))
+
+
+def _bytes(fn, name, t, dev):
+    """(address, bytes) of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        _bad(fn, f"{name}: a contiguous tensor on cuda:{dev} wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run8(fn, dev, stream, *args):
+    """The C call `fn` on device `dev`, its stream last."""
+    import torch
+
+    if dev < 0:
+        _bad(fn, "CUDA tensors wanted")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == dev:
+        st = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, stream)
+    if st != IQ_OK:
+        raise IqError(fn, st)
+
+
+def iq_cache8_bytes(n_layers, n_kv_heads, page_size, n_pages):
+    a = ctypes.c_size_t(0)
+    _check("iq_cache8_bytes", lib().iq_cache8_bytes(n_layers, n_kv_heads, page_size, n_pages, ctypes.byref(a)))
+    return a.value
+
+
+class PagedCache8:
+    """Device pool of an 8-bit K/V cache (one torch tensor of tile records) and the iq_cache8 struct over
+    it.  page_size, n_pages and block_table as for PagedCache; code "e4m3" or "s8" (or its IQ_* value);
+    pool: the uint8 tensor to use instead of a new one."""
+
+    def __init__(self, n_layers, n_kv_heads, page_size, n_pages, block_table=None, device="cuda", code="e4m3", pool=None):
+        import torch
+
+        need = iq_cache8_bytes(n_layers, n_kv_heads, page_size, n_pages)
+        if pool is None:
+            pool = torch.empty(need, dtype=torch.uint8, device=device)
+        self.dev = pool.get_device()
+        _plain("PagedCache8", "pool", pool, self.dev, torch.uint8, (need,))
+        self.pool, self.block_table = pool, block_table
+        self.code = CODES8.get(code, code)
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self.n_layers, self.n_kv_heads, self.page_size, self.n_pages = n_layers, n_kv_heads, page_size, n_pages
+        self.max_pages_per_seq = 1
+        table = None
+        if block_table is not None:
+            if block_table.dim() != 2:
+                _bad("PagedCache8", "block_table: [batch][max_pages_per_seq] wanted")
+            self.max_pages_per_seq = int(block_table.shape[1])
+            table = _plain("PagedCache8", "block_table", block_table, self.dev, torch.int32, tuple(block_table.shape))
+        self.max_batch = n_pages if block_table is None else int(block_table.shape[0])
+        self.c = iq_cache8(pool.data_ptr(), n_layers, n_kv_heads, HEAD_DIM, page_size, n_pages, table,
+                           self.max_pages_per_seq, self.status.data_ptr(), self.code)
+        self.ref = ctypes.byref(self.c)
+
+    def tiles(self):
+        """[L][n_pages][Hkv][page_size/32][8224] tile records."""
+        return self.pool.view(self.n_layers, self.n_pages, self.n_kv_heads, self.page_size // TILE_TOKENS, TILE8_BYTES)
+
+
+def _batch8(fn, cache, batch):
+    if batch > cache.max_batch:
+        _bad(fn, f"{batch} sequences, and rows for {cache.max_batch} in the cache")
+
+
+def iq_append8(cache, layer, k, v, start_pos, n_valid=None, stream=None):
+    """k, v: fp16, bf16 or fp32 [batch][n_new][Hkv][128] CUDA tensors (either may be None), whose heads are
+    contiguous and whose tokens are equally far apart (slices of a fused projection's rows are); start_pos,
+    n_valid: int32 [batch]."""
+    fn, dev = "iq_append8", cache.dev
+    x = k if k is not None else v
+    if x is None:
+        _bad(fn, "k or v wanted")
+    batch, n = x.shape[0], x.shape[1]
+    _batch8(fn, cache, batch)
+    if batch == 0 or n == 0:
+        return
+    strides = []
+    for t in (k, v):
+        if t is None:
+            strides.append(0)
+            continue
+        stride = t.stride(1) if n > 1 else t.stride(0) if batch > 1 else 0
+        if (t.dtype != x.dtype or t.get_device() != dev or tuple(t.shape) != (batch, n, cache.n_kv_heads, HEAD_DIM)
+                or t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != HEAD_DIM)
+                or (batch > 1 and t.stride(0) != n * stride)):
+            _bad(fn, f"[{batch}][{n}][{cache.n_kv_heads}][128] tensors of one type, with contiguous heads and equally "
+                     f"distant tokens, on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+        strides.append(stride)
+    _run8(fn, dev, stream, cache.ref, layer, k.data_ptr() if k is not None else None,
+          v.data_ptr() if v is not None else None, _dtype(fn, x), *strides, batch, n,
+          _i32(fn, "start_pos", start_pos, dev, batch),
+          None if n_valid is None else _i32(fn, "n_valid", n_valid, dev, batch))
+
+
+def iq_decode8_workspace_size(batch, n_q_heads, n_kv_heads, max_ctx):
+    return int(lib().iq_decode8_workspace_size(batch, n_q_heads, n_kv_heads, max_ctx))
+
+
+def iq_decode8_attention(cache, layer, q, ctx_len, max_ctx, out, workspace, scale=None, stream=None):
+    """q, out: [batch][Hq][128], fp16, bf16 or fp32; ctx_len: int32 [batch]; workspace: zero-filled before its
+    first use, as iq_decode_attention's; scale: of the scores, 1/sqrt(128) by default."""
+    fn, dev = "iq_decode8_attention", cache.dev
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM:
+        _bad(fn, "q: [batch][Hq][128] wanted")
+    shape = tuple(q.shape)
+    _batch8(fn, cache, shape[0])
+    if q.numel() == 0:
+        return
+    ws, nbytes = _bytes(fn, "workspace", workspace, dev)
+    _run8(fn, dev, stream, cache.ref, layer, _plain(fn, "q", q, dev, q.dtype, shape), _dtype(fn, q), shape[0], shape[1],
+          _i32(fn, "ctx_len", ctx_len, dev, shape[0]), max_ctx, HEAD_DIM ** -0.5 if scale is None else scale,
+          _plain(fn, "out", out, dev, q.dtype, shape), ws, nbytes)
+
+
+def iq_prefill8_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, max_ctx):
+    return int(lib().iq_prefill8_workspace_size(batch, n_tokens, n_q_heads, n_kv_heads, max_ctx))
+
+
+def iq_prefill8_attention(cache, layer, q, start_pos, max_ctx, out, workspace, n_valid=None, scale=None, stream=None):
+    """q, out: [batch][n_tokens][Hq][128], fp16, bf16 or fp32; query token i of sequence b at position start_pos[b]
+    + i attends causally; n_valid: int32 [batch], the tokens that are there (rows of out behind them stay as they
+    were)."""
+    fn, dev = "iq_prefill8_attention", cache.dev
+    if q.dim() != 4 or q.shape[3] != HEAD_DIM:
+        _bad(fn, "q: [batch][n_tokens][Hq][128] wanted")
+    shape = tuple(q.shape)
+    _batch8(fn, cache, shape[0])
+    if q.numel() == 0:
+        return
+    ws, nbytes = _bytes(fn, "workspace", workspace, dev)
+    _run8(fn, dev, stream, cache.ref, layer, _plain(fn, "q", q, dev, q.dtype, shape), _dtype(fn, q), shape[0], shape[1],
+          shape[2], _i32(fn, "start_pos", start_pos, dev, shape[0]),
+          None if n_valid is None else _i32(fn, "n_valid", n_valid, dev, shape[0]), max_ctx,
+          HEAD_DIM ** -0.5 if scale is None else scale, _plain(fn, "out", out, dev, q.dtype, shape), ws, nbytes)
+
+
+def iq_export8(cache, layer, kv, seq, t0, n, values, stream=None):
+    """values: float32 [Hkv][n][128] CUDA tensor."""
+    import torch
+
+    fn = "iq_export8"
+    if seq >= cache.max_batch:
+        _bad(fn, f"sequence {seq}, and rows for {cache.max_batch} in the cache")
+    if n == 0:
+        return
+    _run8(fn, cache.dev, stream, cache.ref, layer, kv, seq, t0, n,
+          _plain(fn, "values", values, cache.dev, torch.float32, (cache.n_kv_heads, n, HEAD_DIM)))
+
+
+def iq_rope_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, low=1.0, high=32.0):
+    """(float64 [rotary_dim/2] radians per position, factor on q and k); scalings as in include/iq.h."""
+    out, ms = np.zeros(max(0, rotary_dim // 2), dtype=np.float64), ctypes.c_double(0.0)
+    _check("iq_rope_frequencies", lib().iq_rope_frequencies(
+        rotary_dim, base, ROPE_SCALINGS.get(scaling, scaling), factor, original_len, low, high,
+        out.ctypes.data_as(ctypes.c_void_p), ctypes.byref(ms)))
+    return out, ms.value
+
+
+def _rope_side(fn, name, x, y, dtype, dev, n):
+    """(address, row stride, out address, out row stride, heads) of q or k."""
+    if x is None or y is None:
+        if x is not None or y is not None:
+            _bad(fn, f"{name} and {name}_out belong together")
+        return None, 0, None, 0, 0
+    heads = x.shape[1] if x.dim() == 3 else 0
+    for t in (x, y):
+        if (t.dtype != dtype or t.get_device() != dev or tuple(t.shape) != (n, heads, HEAD_DIM) or t.stride(2) != 1
+                or (heads > 1 and t.stride(1) != HEAD_DIM)):
+            _bad(fn, f"{name}: [{n}][heads][128] tensors of one type with contiguous heads on cuda:{dev} wanted, got "
+                     f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    if n < 2:
+        return x.data_ptr(), 0, y.data_ptr(), 0, heads
+    return x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), heads
+
+
+def iq_rope(q, k, positions, freq, q_out=None, k_out=None, layout="half", mscale=1.0, inverse=False, stream=None):
+    """q, k: fp16, bf16 or fp32 [n_tokens][heads][128] (either may be None), rows as far apart as they may be;
+    q_out, k_out: where the results go, by default q and k themselves; positions: int32 [n_tokens]; freq:
+    float64 [rotary_dim/2] (iq_rope_frequencies)."""
+    import torch
+
+    fn = "iq_rope"
+    x = q if q is not None else k
+    if x is None:
+        _bad(fn, "q or k wanted")
+    dev, n, pairs = x.get_device(), x.shape[0], freq.numel()
+    if n == 0:
+        return
+    a = _rope_side(fn, "q", q, q if q_out is None else q_out, x.dtype, dev, n)
+    b = _rope_side(fn, "k", k, k if k_out is None else k_out, x.dtype, dev, n)
+    _run8(fn, dev, stream, *a[:4], *b[:4], _dtype(fn, x), n, a[4], b[4], 2 * pairs, ROPE_LAYOUTS.get(layout, layout),
+          _i32(fn, "positions", positions, dev, n), _plain(fn, "freq", freq, dev, torch.float64, (pairs,)), mscale,
+          1 if inverse else 0)
+
+
+class PageTable:
+    """Block table, lengths and page counts of up to max_seqs sequences (give .block_table to the caches), and
+    the workspace of the operations on them.  Tensors given are used as they are."""
+
+    def __init__(self, max_seqs, max_pages_per_seq, page_size, n_pages, device="cuda", block_table=None, seq_len=None,
+                 ref=None):
+        import torch
+
+        if block_table is None:
+            block_table = torch.full((max_seqs, max_pages_per_seq), -1, dtype=torch.int32, device=device)
+        device = block_table.device
+        if seq_len is None:
+            seq_len = torch.zeros(max_seqs, dtype=torch.int32, device=device)
+        if ref is None:
+            ref = torch.zeros(n_pages, dtype=torch.int32, device=device)
+        self.dev = block_table.get_device()
+        self.block_table, self.seq_len, self.ref = block_table, seq_len, ref
+        self.page_size, self.n_pages = page_size, n_pages
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.c = iq_pages(
+            _plain("PageTable", "block_table", block_table, self.dev, torch.int32, (max_seqs, max_pages_per_seq)),
+            _i32("PageTable", "seq_len", seq_len, self.dev, max_seqs), _i32("PageTable", "ref", ref, self.dev, n_pages),
+            max_seqs, max_pages_per_seq, page_size, n_pages, self.status.data_ptr())
+        self.p = ctypes.byref(self.c)
+        need = int(lib().iq_pages_workspace_size(self.p))
+        if not need:
+            _bad("PageTable", "sizes of at least 1 and a page_size that is a multiple of 32 wanted")
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self.ws = self.workspace.data_ptr(), need
+
+
+class PagePool:
+    """The pool of a cache (or several: PagePool.of(cache, ...)) whose pages a PageTable's operations move."""
+
+    def __init__(self, pool, n_layers, n_kv_heads, page_size, n_pages, tile_bytes):
+        import torch
+
+        self.page_size, self.n_pages, self.n, self.dev = page_size, n_pages, 1, pool.get_device()
+        self.held = [pool]
+        need = n_layers * n_pages * n_kv_heads * (page_size // TILE_TOKENS) * tile_bytes
+        addr = _plain("PagePool", "pool", pool, self.dev, torch.uint8, (need,))
+        self.c = (iq_page_pool * 1)(iq_page_pool(addr, n_layers, n_kv_heads, tile_bytes))
+
+    @classmethod
+    def of(cls, *caches):
+        """The pools of caches of either kind that share a block table."""
+        if not caches:
+            _bad("PagePool", "a cache wanted")
+        each = [cls(c.pool, c.n_layers, c.n_kv_heads, c.page_size, c.n_pages, getattr(c, "tile_bytes", TILE8_BYTES))
+                for c in caches]
+        one = each[0]
+        if any((e.page_size, e.n_pages, e.dev) != (one.page_size, one.n_pages, one.dev) for e in each):
+            _bad("PagePool", "caches of one page size, number of pages and device wanted")
+        one.n, one.held = len(each), [e.held[0] for e in each]
+        one.c = (iq_page_pool * len(each))(*(e.c[0] for e in each))
+        return one
+
+
+def _pools(fn, table, pools):
+    if pools is None:
+        return None, 0
+    if (pools.page_size, pools.n_pages, pools.dev) != (table.page_size, table.n_pages, table.dev):
+        _bad(fn, "the pools' page size, number of pages and device are not the table's")
+    return pools.c, pools.n
+
+
+def iq_pages_extend(table, ids, new_len, stream=None):
+    """Sequences ids grow to new_len tokens (int32 [n] each) and get their pages."""
+    fn, n = "iq_pages_extend", ids.numel()
+    _run8(fn, table.dev, stream, table.p, _i32(fn, "ids", ids, table.dev, n), _i32(fn, "new_len", new_len, table.dev, n), n,
+          *table.ws)
+
+
+def iq_pages_free(table, ids, stream=None):
+    fn, n = "iq_pages_free", ids.numel()
+    _run8(fn, table.dev, stream, table.p, _i32(fn, "ids", ids, table.dev, n), n)
+
+
+def iq_pages_fork(table, pools, parent, child, stream=None):
+    """Empty sequences child become copies of parent (int32 [n] each); pools: a PagePool, or None."""
+    fn, n = "iq_pages_fork", parent.numel()
+    c, m = _pools(fn, table, pools)
+    _run8(fn, table.dev, stream, table.p, c, m, _i32(fn, "parent", parent, table.dev, n),
+          _i32(fn, "child", child, table.dev, n), n, *table.ws)
+
+
+def iq_pages_compact(table, pools, n_held=None, stream=None):
+    """The held pages move to the front; n_held: int32 [1] that gets their number, or None."""
+    fn = "iq_pages_compact"
+    c, m = _pools(fn, table, pools)
+    _run8(fn, table.dev, stream, table.p, c, m, None if n_held is None else _i32(fn, "n_held", n_held, table.dev, 1),
+          *table.ws)
+
+
+def iq_pages_copy(table, pools, src, dst, stream=None):
+    """Page src[i] of every layer to page dst[i] (int32 [n] each)."""
+    fn, n = "iq_pages_copy", src.numel()
+    c, m = _pools(fn, table, pools)
+    _run8(fn, table.dev, stream, table.p, c, m, _i32(fn, "src", src, table.dev, n), _i32(fn, "dst", dst, table.dev, n), n,
+          *table.ws)

@@ -1,0 +1,252 @@
+// Quantise-and-append into the 8-bit cache, and its read-back.
+//
+// One warp owns the K or the V half of one tile record (32 tokens of one sequence and kv head) that
+// gets new tokens: it finds the largest finite magnitude, hence the block's scale; re-rounds the codes
+// of the tokens that were there if the scale grew; writes the new tokens' codes.  Powers of two
+// (e4m3) and scales of 8 significant bits (int8) make every quotient below correctly rounded, so that
+// the result does not depend on how the tokens were split over calls, apart from that re-rounding.
+// Bound by memory: 512 B in and 257 B out for each token and kv head.
+#include <math_constants.h>
+
+#include <type_traits>
+
+#include "iq_cache8.cuh"
+
+namespace iq {
+
+constexpr int AP8_WARPS = 8;
+
+struct Append8Args {
+  View8 v;
+  const void *k, *v_new;
+  long long ks, vs;  // elements from a token's row to the next
+  int batch, n_new, tiles;  // tiles: the most that n_new tokens can touch
+  const int32_t* start;
+  const int32_t* n_valid;
+};
+
+// The scale that a block with largest magnitude amax (float32 bits, finite) asks for.
+template <int CODE>
+__device__ __forceinline__ float scale_for(uint32_t amax) {
+  if constexpr (CODE == IQ_E4M3) {
+    // amax <= 448 2^e = 1.75 * 2^(8 + e): e = exponent - 8, one more above a mantissa of 1.75
+    int e = (int)(amax >> 23) - 127 - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    e = amax < 0x00800000u ? -100 : max(-100, min(120, e));
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+  } else {
+    const float s = fmaxf(__fdiv_rn(__uint_as_float(amax), 127.f), 7.888609052210118e-31f);  // 2^-100
+    return __uint_as_float((__float_as_uint(s) + 0xFFFFu) & 0xFFFF0000u);
+  }
+}
+
+// Codes of x0, x1 (low byte first) under a scale; NaN -> 0, saturating.
+template <int CODE>
+__device__ __forceinline__ uint32_t quantise2(float x0, float x1, float scale, float inv) {
+  x0 = x0 == x0 ? x0 : 0.f;
+  x1 = x1 == x1 ? x1 : 0.f;
+  if constexpr (CODE == IQ_E4M3) {
+    uint32_t r;  // the product with a power of two is exact, the conversion the one rounding
+    asm("{\n .reg .b16 t;\n cvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n cvt.u32.u16 %0, t;\n}\n"
+        : "=r"(r)
+        : "f"(x0 * inv), "f"(x1 * inv));
+    return r;
+  } else {
+    const float a = fminf(fmaxf(rintf(__fdiv_rn(x0, scale)), -127.f), 127.f);
+    const float b = fminf(fmaxf(rintf(__fdiv_rn(x1, scale)), -127.f), 127.f);
+    return ((uint32_t)(int)a & 0xFFu) | (((uint32_t)(int)b & 0xFFu) << 8);
+  }
+}
+
+// Eight values of one row as float32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float f[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen8(uint4 u, float f[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+  const uint32_t a = __float_as_uint(x) & 0x7FFFFFFFu;
+  return a < 0x7F800000u ? a : 0u;
+}
+
+// Lanes 0-15 take row 2 i, lanes 16-31 row 2 i + 1, eight coordinates each: 16-byte loads (16-bit
+// types) of whole 256-byte rows, 8-byte stores.
+template <int CODE, typename T>
+__global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31, c8 = lane & 15, odd = lane >> 4;
+  // unit = ((sequence, tile), side, head), heads fastest: neighbouring warps read neighbouring rows
+  long long u = (long long)blockIdx.x * AP8_WARPS + (threadIdx.x >> 5);
+  const int head = (int)(u % a.v.n_kv_heads);
+  u /= a.v.n_kv_heads;
+  const int side = (int)(u & 1);
+  u >>= 1;
+  const int j = (int)(u % a.tiles), b = (int)(u / a.tiles);
+  const T* const x = (const T*)(side ? a.v_new : a.k);
+  const long long stride = side ? a.vs : a.ks;
+  if (b >= a.batch || !x) return;
+  int cnt = a.n_valid ? a.n_valid[b] : a.n_new;
+  uint32_t err = 0;
+  if (cnt < 0 || cnt > a.n_new) {
+    err |= IQ_DEVERR_CTX;
+    cnt = cnt < 0 ? 0 : a.n_new;
+  }
+  const long long start = a.start[b];
+  const long long t0 = ((start >> 5) + j) * TILE_TOKENS;  // position of the tile's first slot
+  const long long first = max(start, t0), end = min(start + cnt, t0 + TILE_TOKENS);
+  int page = -1;
+  if (first < end) page = find_page8(a.v, b, t0, &err);
+  if (err && a.v.status && lane == 0) atomicOr(a.v.status, err);
+  if (page < 0) return;
+  uint8_t* const rec = tile_record8(a.v, page, head, (int)(t0 % a.v.page_size));
+  uint8_t* const rows = rec + side * TILE8_V;
+  float* const sc = reinterpret_cast<float*>(rec + TILE8_SCALES) + side;
+  const int lo = (int)(first - t0), hi = (int)(end - t0);  // the new tokens' rows
+  const T* const src = x + ((long long)b * a.n_new + (t0 - start)) * stride + head * D + 8 * c8;
+
+  // largest finite magnitude, and the rows themselves where they fit the registers
+  constexpr bool KEEP = sizeof(T) == 2;
+  uint4 raw[KEEP ? 16 : 1];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + odd;
+    if constexpr (KEEP) {
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (r >= lo && r < hi) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + odd;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if constexpr (KEEP) widen8<T>(raw[i], f);
+    else if (r >= lo && r < hi) load8(src + r * stride, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = max(amax, finite_magnitude(f[k]));
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  float scale = scale_for<CODE>(amax);
+  float was = lo > 0 ? *sc : 0.f;  // tokens before the new ones: their scale stays or grows
+  was = was > 0.f && was < CUDART_INF_F ? was : 0.f;
+  const bool grew = lo > 0 && scale > was;
+  if (lo > 0 && !grew) scale = was;
+  const float inv = CODE == IQ_E4M3 ? 1.f / scale : 0.f;  // exact: a power of two
+  __syncwarp();
+  if (lane == 0) *sc = scale;
+  if (grew) {
+    for (int r = odd; r < lo; r += 2) {
+      uint2* p = reinterpret_cast<uint2*>(rows + chunk8(r, c8 >> 1) + 8 * (c8 & 1));
+      const uint2 w = *p;
+      uint32_t o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x, y;
+        codes4_to_half2x2<CODE>(h ? w.y : w.x, x, y);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&y));
+        o[h] = quantise2<CODE>(f.x * was, f.y * was, scale, inv) | (quantise2<CODE>(g.x * was, g.y * was, scale, inv) << 16);
+      }
+      *p = make_uint2(o[0], o[1]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + odd;
+    if (r < lo || r >= hi) continue;
+    float f[8];
+    if constexpr (KEEP) widen8<T>(raw[i], f);
+    else load8(src + r * stride, f);
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      o[h] = quantise2<CODE>(f[4 * h], f[4 * h + 1], scale, inv) |
+             (quantise2<CODE>(f[4 * h + 2], f[4 * h + 3], scale, inv) << 16);
+    *reinterpret_cast<uint2*>(rows + chunk8(r, c8 >> 1) + 8 * (c8 & 1)) = make_uint2(o[0], o[1]);
+  }
+}
+
+int launch_append8(const View8& v, const void* k, const void* vsrc, int dtype, long long ks, long long vs, int batch, int n_new,
+                   const int32_t* start, const int32_t* n_valid, void* stream) {
+  if (batch == 0 || n_new == 0) return 0;
+  Append8Args a;
+  a.v = v;
+  a.k = k;
+  a.v_new = vsrc;
+  a.ks = ks;
+  a.vs = vs;
+  a.batch = batch;
+  a.n_new = n_new;
+  a.tiles = (n_new + 2 * TILE_TOKENS - 2) / TILE_TOKENS;
+  a.start = start;
+  a.n_valid = n_valid;
+  const long long units = (long long)batch * a.tiles * 2 * v.n_kv_heads;
+  const long long blocks = (units + AP8_WARPS - 1) / AP8_WARPS;
+  if (blocks > 0x7FFFFFFFll) return (int)cudaErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(AP8_WARPS * 32);
+  const cudaStream_t st = (cudaStream_t)stream;
+  const bool e4 = v.code == IQ_E4M3;
+  if (dtype == IQ_F16)
+    return (int)(e4 ? launch_pdl(append8_kernel<IQ_E4M3, __half>, grid, block, 0, st, a)
+                    : launch_pdl(append8_kernel<IQ_S8, __half>, grid, block, 0, st, a));
+  if (dtype == IQ_BF16)
+    return (int)(e4 ? launch_pdl(append8_kernel<IQ_E4M3, __nv_bfloat16>, grid, block, 0, st, a)
+                    : launch_pdl(append8_kernel<IQ_S8, __nv_bfloat16>, grid, block, 0, st, a));
+  return (int)(e4 ? launch_pdl(append8_kernel<IQ_E4M3, float>, grid, block, 0, st, a)
+                  : launch_pdl(append8_kernel<IQ_S8, float>, grid, block, 0, st, a));
+}
+
+// One thread per (kv head, token, 16-byte chunk): code * scale.
+__global__ void export8_kernel(View8 v, int kv, int seq, int t0, int n, float* values) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  const int tok = i >> 3, c = i & 7, head = blockIdx.y;
+  if (tok >= n) return;
+  uint32_t err = 0;
+  const long long pos = (long long)t0 + tok;
+  const int page = find_page8(v, seq, pos, &err);
+  float* const out = values + ((size_t)head * n + tok) * D + 16 * c;
+  if (page < 0) {
+    if (v.status) atomicOr(v.status, err);
+    for (int k = 0; k < 16; ++k) out[k] = __uint_as_float(0x7FC00000u);
+    return;
+  }
+  const int slot = (int)(pos % v.page_size);
+  const uint8_t* rec = tile_record8(v, page, head, slot);
+  const float sc = reinterpret_cast<const float*>(rec + TILE8_SCALES)[kv];
+  const uint8_t* p = rec + kv * TILE8_V + chunk8(slot % TILE_TOKENS, c);
+  for (int k = 0; k < 16; k += 4) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p + k);
+    uint32_t x, y;
+    if (v.code == IQ_E4M3) codes4_to_half2x2<IQ_E4M3>(w, x, y);
+    else codes4_to_half2x2<IQ_S8>(w, x, y);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&y));
+    out[k] = f.x * sc; out[k + 1] = f.y * sc; out[k + 2] = g.x * sc; out[k + 3] = g.y * sc;
+  }
+}
+
+int launch_export8(const View8& v, int kv, int seq, int t0, int n, float* values, void* stream) {
+  if (n == 0) return 0;
+  const dim3 grid((unsigned)(((long long)n * 8 + 127) / 128), v.n_kv_heads);
+  export8_kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(v, kv, seq, t0, n, values);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace iq
