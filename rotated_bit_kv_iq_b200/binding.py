@@ -1,4 +1,4 @@
-"""ctypes binding of libiq (include/iq.h): argument marshalling only.
+"""ctypes binding of libiq (include/iq.h, include/iq8.h): argument marshalling only.
 
 Every entry point keeps its C name.  Device buffers are torch CUDA tensors (PyTorch is used
 for device memory and streams only); every step of the computation runs in libiq's kernels.
@@ -606,7 +606,7 @@ def iq_export8(cache, layer, kv, seq, t0, n, values, stream=None):
 
 
 def iq_rope_frequencies(rotary_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, low=1.0, high=32.0):
-    """(float64 [rotary_dim/2] radians per position, factor on q and k); scalings as in include/iq.h."""
+    """(float64 [rotary_dim/2] radians per position, factor on q and k); scalings as in include/iq8.h."""
     out, ms = np.zeros(max(0, rotary_dim // 2), dtype=np.float64), ctypes.c_double(0.0)
     _check("iq_rope_frequencies", lib().iq_rope_frequencies(
         rotary_dim, base, ROPE_SCALINGS.get(scaling, scaling), factor, original_len, low, high,

@@ -27,7 +27,7 @@ def _nvcc():
 
 def _newest_source_mtime():
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    paths.append(os.path.join(HERE, "..", "include", "iq.h"))
+    paths += [os.path.join(HERE, "..", "include", f) for f in ("iq.h", "iq8.h")]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths if os.path.exists(p))
 

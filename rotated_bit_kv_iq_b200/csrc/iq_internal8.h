@@ -3,6 +3,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "../../include/iq8.h"
 #include "iq_internal.h"
 
 namespace iq {

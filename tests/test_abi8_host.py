@@ -2,6 +2,8 @@
 host-only calls, and what the binding refuses of tensors."""
 
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -33,6 +35,15 @@ BAD_CACHES = [(dict(head_dim=64), B.IQ_ERR_UNSUPPORTED), (dict(page_size=24), B.
               (dict(code=2), B.IQ_ERR_UNSUPPORTED), (dict(code=-1), B.IQ_ERR_UNSUPPORTED),
               (dict(n_layers=0), B.IQ_ERR_INVALID_ARG), (dict(status_dev=0x10001), B.IQ_ERR_ALIGNMENT),
               (dict(block_table_dev=0xB0000, max_pages_per_seq=0), B.IQ_ERR_INVALID_ARG)]
+
+
+def test_library_exports_every_declared_symbol(lib):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    hdr = open(os.path.join(root, "include", "iq8.h")).read()
+    names = set(re.findall(r"^[A-Za-z_][\w\s\*]*?\b(iq_\w+)\s*\(", hdr, flags=re.M))
+    assert len(names) == 15
+    for n in names:
+        assert hasattr(lib, n) and hasattr(B, n) or n == "iq_pages_workspace_size", n
 
 
 def test_cache8_bytes(lib):
