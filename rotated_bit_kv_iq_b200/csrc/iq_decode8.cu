@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __shared__ int s_start[2];  // the CTA's first sequence, and the tiles before it within all kv heads
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
-  const int Hkv = a.v.n_kv_heads, G = a.g_real, N = gridDim.x, c = blockIdx.x;
+  const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
   float* const so = reinterpret_cast<float*>(smem + D8_RING);
   if (lane == 0) {
     for (int i = 0; i < D8_NB; ++i) mbar_init(&bars[warp][i], 1);
@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   }
   before *= Hkv;
   total *= Hkv;
-  const long long lo = c * total / N, hi = (c + 1) * total / N;
+  // the CTAs that share the tiles: none without one, and no more than give every warp one
+  const int N = (int)min((long long)gridDim.x, max(1ll, (total + D8_WARPS - 1) / D8_WARPS));
+  const long long lo = c < N ? c * total / N : total, hi = c < N ? (c + 1) * total / N : total;
   long long acc = before;  // tiles of all groups before sequence b
   for (int b = b0; b < min(a.batch, b0 + per); ++b) {
     const long long nt = (long long)Hkv * ((clamp_ctx8(a, b) + TILE_TOKENS - 1) / TILE_TOKENS);
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     for (int b = tid; b < a.batch; b += D8_THREADS)
       if (clamp_ctx8(a, b) != a.ctx_len[b]) atomicOr(a.v.status, IQ_DEVERR_CTX);
   // sequences with nothing to see: zero rows
-  for (int b = c; b < a.batch; b += N)
+  for (int b = c; b < a.batch; b += gridDim.x)
     if (clamp_ctx8(a, b) == 0)
       for (int i = tid; i < a.n_q_heads * (D / 4); i += D8_THREADS)
         store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));

@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "iq_attend8.cuh"
+#include "iq_prefill8_tc.cuh"
 
 namespace iq {
 
@@ -90,11 +91,15 @@ __global__ void __launch_bounds__(P8_WARPS * 32) prefill8_kernel(Prefill8Args a)
   }
 }
 
-size_t prefill8_workspace_bytes(int, int, int, int, int) { return 256; }
+size_t prefill8_workspace_bytes(int batch, int n_tok, int n_q_heads, int n_kv_heads, int max_ctx) {
+  return pt_plan(batch, n_tok, std::min(8, n_q_heads / n_kv_heads), n_kv_heads, max_ctx).bytes;
+}
 
 int launch_prefill8(const View8& v, const void* q, int dtype, int batch, int n_tok, int n_q_heads, const int32_t* start,
-                    const int32_t* n_valid, int max_ctx, float scale, void* out, void*, void* stream) {
+                    const int32_t* n_valid, int max_ctx, float scale, void* out, void* workspace, void* stream) {
   if (batch == 0 || n_tok == 0) return 0;
+  if (dtype != IQ_F32)
+    return launch_prefill8_tc(v, q, dtype, batch, n_tok, n_q_heads, start, n_valid, max_ctx, scale, out, workspace, stream);
   Prefill8Args a;
   a.v = v;
   a.q = q;

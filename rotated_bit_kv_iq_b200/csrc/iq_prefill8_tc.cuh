@@ -1,0 +1,619 @@
+// Causal attention of a chunk of 16-bit query tokens over the 8-bit cache on the 5th-generation tensor cores.
+//
+// A block is 256 query rows (256 / G tokens x the G heads of one kv head) as two tiles of 128; it streams the
+// keys in steps of 128 (four tile records).  8-bit codes are exact in binary16, so a step's K and V are expanded
+// once for both tiles into shared memory, and with S in tensor memory:
+//   S = Q K^T       128 x 128 x 128, Q and K in shared memory (both along the coordinates)
+//   O += P V        128 x 128 x 128, P in tensor memory (binary16, over S's own columns), V in shared memory
+//                   as it lies in the cache: rows of coordinates (N-major operand)
+// The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and
+// the V scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is a running maximum
+// of s + log2 v that follows only once it has been passed by 2^8: O is then rescaled in tensor memory, rarely.
+// p' is one binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are
+// float32.
+//
+// Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that
+// neither causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block
+// cut by a run's end leaves partials, which a second kernel merges in order.
+// Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 the expansion, 12 issues the MMAs:
+// while one tile's scores are in the softmax, the tensor core works for the other tile.
+#pragma once
+#include <algorithm>
+
+#include "iq_attend8.cuh"
+#include "iq_tcgen05.cuh"
+
+namespace iq {
+
+constexpr int PT_TILE = 128;  // rows of a tile: the MMA's M
+constexpr int PT_ROWS = 256;  // rows of a block
+constexpr int PT_BN = 128;    // keys of a step
+constexpr int PT_THREADS = 416;
+constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
+constexpr float PT_SLACK = 8.f;
+
+struct PtSmem {
+  static constexpr int q = 0;                 // [tile] 128 rows x 128 coordinates
+  static constexpr int k = 65536;             // [buffer] 128 keys x 128 coordinates
+  static constexpr int v = 131072;            // [buffer]
+  static constexpr int ks = 196608;           // float [4][4]: K scales of step n mod 4's tile records
+  static constexpr int lv = ks + 64;          // float [4][4]: log2 of the V scales; NaN: the record is not there
+  static constexpr int w = lv + 64;           // float [4][4]: 2^(base - log2 of the V scale)
+  static constexpr int base = w + 64;         // float [4]: base of segment mod 4
+  static constexpr int scan = base + 16;      // int64 [13], then the plan: int [4]
+  static constexpr int bars = scan + 128;     // uint64 [TB_COUNT]
+  static constexpr int misc = bars + 20 * 8;  // uint32 tensor-memory base, int abort
+  static constexpr int bytes = misc + 16 + 1024;
+};
+static_assert(PtSmem::bytes <= 232448, "one CTA's shared memory");
+
+// mbarriers: K and V of step parity expanded / free again; per tile: scores ready, P written, O += P V done; queries.
+enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 10, TB_ODONE = 12, TB_Q = 14,
+       TB_DRAIN = 15, TB_COUNT = 16 };
+
+struct PtArgs {
+  View8 v;
+  const void* q;
+  int dtype, batch, n_tok, n_q_heads, g_real, tq, n_blk, max_ctx;
+  const int32_t* start;
+  const int32_t* n_valid;
+  float scale;
+  void* out;
+  int2* cut;        // [batch][n_blk][Hkv]: the first and last CTA of the block
+  float4* part_ml;  // [2 N][256]: (max of scores, max with values' scales, sum)
+  float* part_o;    // [2 N][256][128]
+};
+
+// Bounded wait that also ends once another thread has given up.
+__device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > 1000000000ull) {
+      if (status) atomicOr(status, IQ_DEVERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// Entry e = (sequence, block of tokens): where its rows and keys are.
+struct PtEntry {
+  int b, tok0, n_live, pos0, kv_end, steps;
+};
+__device__ __forceinline__ PtEntry pt_entry(const PtArgs& a, int e) {
+  PtEntry x;
+  x.b = e / a.n_blk;
+  x.tok0 = (e % a.n_blk) * a.tq;
+  int cnt = a.n_valid ? a.n_valid[x.b] : a.n_tok;
+  cnt = max(0, min(a.n_tok, cnt));
+  const int start = max(0, min(a.max_ctx - cnt, a.start[x.b]));
+  x.n_live = max(0, min(a.tq, cnt - x.tok0));
+  x.pos0 = start + x.tok0;
+  x.kv_end = x.pos0 + x.n_live;
+  x.steps = x.n_live ? (x.kv_end + PT_BN - 1) / PT_BN : 0;
+  return x;
+}
+
+// A CTA's run of (block, step) pairs, one segment (steps [k0, k1) of one block) after another.
+struct PtWalk {
+  PtEntry x;
+  long long pos, end;
+  int e, kvh, k0, k1;
+  __device__ __forceinline__ void cut() { k1 = (int)min((long long)x.steps, k0 + (end - pos)); }
+  __device__ __forceinline__ bool next(const PtArgs& a) {  // false at the run's end
+    pos += k1 - k0;
+    if (pos >= end) return false;
+    k0 = 0;
+    if (++kvh == a.v.n_kv_heads) {
+      kvh = 0;
+      do x = pt_entry(a, ++e);
+      while (x.steps == 0);
+    }
+    cut();
+    return true;
+  }
+};
+
+template <int CODE>
+__global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
+  using SM = PtSmem;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + SM::bars);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::misc);
+  volatile int* const abort = reinterpret_cast<volatile int*>(smem + SM::misc + 4);
+  long long* const s_scan = reinterpret_cast<long long*>(smem + SM::scan);
+  int* const s_plan = reinterpret_cast<int*>(smem + SM::scan + 13 * 8);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < TB_COUNT; ++i) {
+      const int count = (i >= TB_KFULL && i < TB_KFULL + 2) || (i >= TB_VFULL && i < TB_VFULL + 2) ? 128
+                        : i >= TB_PFULL && i < TB_PFULL + 2                                        ? 128
+                        : i == TB_Q                                                                ? 256
+                                                                                                   : 1;
+      mbar_init(&bars[i], count);
+    }
+    mbar_fence_init();
+    *abort = 0;
+  }
+  pdl_wait();
+
+  // ---- plan: the total number of steps, this CTA's run, the block that it starts in
+  const int E = a.batch * a.n_blk, per = (E + PT_THREADS - 1) / PT_THREADS, e0 = min(E, tid * per), e1 = min(E, e0 + per);
+  long long mine = 0;
+  for (int e = e0; e < e1; ++e) mine += pt_entry(a, e).steps;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long acc = incl - mine, total = 0;
+  for (int w = 0; w < PT_THREADS / 32; ++w) {
+    if (w < warp) acc += s_scan[w];
+    total += s_scan[w];
+  }
+  acc *= Hkv;
+  total *= Hkv;
+  const int N = (int)min((long long)gridDim.x, total);  // the CTAs that share the steps: none without one
+  if (c >= N && c) return;
+  const long long lo = c * total / max(N, 1), hi = (c + 1) * total / max(N, 1);
+  for (int e = e0; e < e1 && acc <= lo; ++e) {
+    const long long nt = (long long)Hkv * pt_entry(a, e).steps;
+    if (lo < hi && lo < acc + nt) {
+      s_plan[0] = e;
+      s_plan[1] = (int)(lo - acc);
+      break;
+    }
+    acc += nt;
+  }
+  if (c == 0 && a.v.status)  // counts and starts outside their ranges
+    for (int b = tid; b < a.batch; b += PT_THREADS) {
+      const int cnt = a.n_valid ? a.n_valid[b] : a.n_tok, st = a.start[b];
+      if (cnt < 0 || cnt > a.n_tok || st < 0 || st > a.max_ctx - max(0, min(a.n_tok, cnt))) atomicOr(a.v.status, IQ_DEVERR_CTX);
+    }
+  if (lo >= hi) return;
+  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PtWalk s;
+  s.e = s_plan[0];
+  s.x = pt_entry(a, s.e);
+  s.kvh = s_plan[1] / s.x.steps;
+  s.k0 = s_plan[1] % s.x.steps;
+  s.pos = lo;
+  s.end = hi;
+  s.cut();
+
+  if (warp < 8) {
+    // ==== softmax: thread = row r of the block (row r mod 128 of tile t)
+    const int t = warp >> 2, r = 128 * t + 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tS = tmem + lanes + PT_S_COL + 128 * t, tO = tmem + lanes + PT_O_COL + 128 * t;
+    const float* const s_ks = reinterpret_cast<const float*>(smem + SM::ks);
+    const float* const s_lv = reinterpret_cast<const float*>(smem + SM::lv);
+    const float* const s_w = reinterpret_cast<const float*>(smem + SM::w);
+    const float* const s_base = reinterpret_cast<const float*>(smem + SM::base);
+    uint32_t done = 0;  // steps of this tile so far
+    uint32_t n = 0;     // steps of the run so far
+    uint32_t seg = 0;
+    bool ok = true;
+    do {
+      const int tiles = s.x.n_live * G > PT_TILE ? 2 : 1, tok = r / G;
+      const bool live = r < a.tq * G && tok < s.x.n_live;
+      const size_t row = ((size_t)s.x.b * a.n_tok + s.x.tok0 + tok) * a.n_q_heads + (size_t)s.kvh * G + r % G;
+      // queries: scaled by the power of two that brings the row's largest magnitude to [2^14, 2^15)
+      float qs = 1.f;
+      {
+        uint4 u[16];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          u[i] = live ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + row * D) + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = a.dtype == IQ_F16 ? half2_floats(x[j]) : make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+        ex = max(-100, min(126, ex));
+        const float sig = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        if (live) qs = a.scale * kLog2E8 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = a.dtype == IQ_F16 ? half2_floats(x[j]) : make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+            x[j] = half2_bits(f.x * sig, f.y * sig);
+          }
+          *reinterpret_cast<uint4*>(smem + SM::q + 32768 * t + umma_sw128_off(r & 127, 8 * i, PT_TILE)) =
+              make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&bars[TB_Q]);
+      float ref = -CUDART_INF_F, l = 0.f;
+      if (t < tiles) {
+        const int qpos = live ? s.x.pos0 + tok : -1;  // the last key that the row sees
+        for (int i = s.k0; i < s.k1; ++i, ++done) {
+          ok = ok && pt_wait(&bars[TB_SFULL + t], done & 1, abort, a.v.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const int slot = 4 * ((n + i - s.k0) & 3);
+          const int lim = qpos - PT_BN * i;  // keys 0 .. lim of the step
+          float f[4], lv[4];
+          bool there = true;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            f[b] = s_ks[slot + b] * qs;
+            lv[b] = s_lv[slot + b];
+            there = there && lv[b] == lv[b];
+          }
+          const bool full = __all_sync(0xffffffffu, lim >= PT_BN - 1) && there;
+          float mo = -CUDART_INF_F;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t x[32];
+            tmem_ld32(tS + 32 * b, x);
+            tmem_wait_ld();
+            float mx = -CUDART_INF_F;
+            if (full) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
+            } else if (lv[b] == lv[b]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, 32 * b + k <= lim ? __uint_as_float(x[k]) : -CUDART_INF_F);
+            }
+            if (mx > -CUDART_INF_F) mo = fmaxf(mo, fmaf(mx, f[b], lv[b]));
+          }
+          if (i == s.k0) {
+            ref = mo;
+          } else {
+            const bool up = mo > ref + PT_SLACK;
+            if (__any_sync(0xffffffffu, up)) {
+              ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + t], (done - 1) & 1, abort, a.v.status));
+              if (!ok) break;
+              tc_fence_after();
+              const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
+              if (up) ref = mo;
+              l *= al;
+#pragma unroll
+              for (int b = 0; b < 8; ++b) {
+                uint32_t x[16];
+                tmem_ld16(tO + 16 * b, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
+                tmem_st16(tO + 16 * b, x);
+              }
+            }
+          }
+          const float at = ref == -CUDART_INF_F ? 0.f : ref;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t x[32], p[16];
+            tmem_ld32(tS + 32 * b, x);
+            tmem_wait_ld();
+            const float add = lv[b] - at;
+            float sum = 0.f;
+            if (full) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float p0 = fast_exp2(fmaf(__uint_as_float(x[k]), f[b], add));
+                const float p1 = fast_exp2(fmaf(__uint_as_float(x[k + 1]), f[b], add));
+                sum += p0 + p1;
+                p[k / 2] = half2_bits(p0, p1);
+              }
+              l = fmaf(sum, s_w[slot + b], l);
+            } else if (lv[b] == lv[b]) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float p0 = 32 * b + k <= lim ? fast_exp2(fmaf(__uint_as_float(x[k]), f[b], add)) : 0.f;
+                const float p1 = 32 * b + k + 1 <= lim ? fast_exp2(fmaf(__uint_as_float(x[k + 1]), f[b], add)) : 0.f;
+                sum += p0 + p1;
+                p[k / 2] = half2_bits(p0, p1);
+              }
+              l = fmaf(sum, s_w[slot + b], l);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) p[k] = 0u;
+            }
+            tmem_st16(tS + 16 * b, p);  // P over the columns of S that are already used up
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars[TB_PFULL + t]);
+        }
+        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + t], (done - 1) & 1, abort, a.v.status));
+        if (!ok) break;
+        tc_fence_after();
+        const bool whole = s.k0 == 0 && s.k1 == s.x.steps;
+        const float base = s_base[seg & 3];
+        const float inv = l > 0.f ? fast_exp2(base) / l : (l == l ? 0.f : l);
+        const size_t prow = (size_t)(2 * c + (s.pos == lo ? 0 : 1)) * PT_ROWS + r;
+        if (!whole) a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f) : make_float4(ref - base, ref, l, 0.f);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          uint32_t x[16];
+          tmem_ld16(tO + 16 * b, x);
+          tmem_wait_ld();
+          if (!live) continue;
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+            if (whole) store4(a.out, a.dtype, row * D + 16 * b + k, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+            else *reinterpret_cast<float4*>(a.part_o + prow * D + 16 * b + k) = y;
+          }
+        }
+        tc_fence_before();
+      } else {  // no row of this tile: not ahead of the tile that has rows
+        ok = ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      n += s.k1 - s.k0;
+      ++seg;
+    } while (s.next(a));
+  } else if (warp < 12) {
+    // ==== expansion: eight lanes to a 128-byte row of codes; keys 16 j + (e / 8), j = 0 .. 7
+    const int e = tid - 256, p8 = e & 7, r16 = e >> 3;
+    const int ch = p8 ^ (r16 & 7);  // the 16 coordinates that this thread's 16 bytes hold
+    float* const s_ks = reinterpret_cast<float*>(smem + SM::ks);
+    float* const s_lv = reinterpret_cast<float*>(smem + SM::lv);
+    float* const s_w = reinterpret_cast<float*>(smem + SM::w);
+    float* const s_base = reinterpret_cast<float*>(smem + SM::base);
+    // the two binary16 chunks: the halves of the lanes start with different ones, so that eight lanes of a row
+    // never meet in a bank
+    const int first = (ch >> 2) & 1;
+    const uint32_t off0 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3) + first) ^ (r16 & 7)) << 4);
+    const uint32_t off1 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3) + 1 - first) ^ (r16 & 7)) << 4);
+    const uint8_t* rec[4];
+    uint4 rk[8], rv[8];
+    float2 sc = make_float2(0.f, 0.f);
+    int step = s.k0;
+    bool more = true;
+    auto locate = [&]() {  // the records of the step
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int at = PT_BN * step + TILE_TOKENS * b;
+        rec[b] = nullptr;
+        if (at < s.x.kv_end) {
+          uint32_t err = 0;
+          const int page = find_page8(a.v, s.x.b, at, &err);
+          if (page >= 0) rec[b] = tile_record8(a.v, page, s.kvh, at % a.v.page_size);
+          else if (e == 0 && a.v.status) atomicOr(a.v.status, err);
+        }
+      }
+    };
+    auto load = [&](uint4 (&u)[8], int side) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = 16 * j + r16;
+        u[j] = make_uint4(0, 0, 0, 0);
+        if (rec[j >> 1] && PT_BN * step + key < s.x.kv_end)
+          u[j] = __ldg(reinterpret_cast<const uint4*>(rec[j >> 1] + side * TILE8_V + (16 * (j & 1) + r16) * D + 16 * p8));
+      }
+    };
+    auto load_scales = [&]() {
+      sc = make_float2(0.f, __uint_as_float(0x7FC00000u));
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (e == b && rec[b]) sc = *reinterpret_cast<const float2*>(rec[b] + TILE8_SCALES);
+    };
+    auto expand = [&](const uint4 (&u)[8], uint8_t* dst) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint4 x, y;
+        codes4_to_half2x2<CODE>(u[j].x, x.x, x.y);
+        codes4_to_half2x2<CODE>(u[j].y, x.z, x.w);
+        codes4_to_half2x2<CODE>(u[j].z, y.x, y.y);
+        codes4_to_half2x2<CODE>(u[j].w, y.z, y.w);
+        *reinterpret_cast<uint4*>(dst + off0 + 2048 * j) = first ? y : x;
+        *reinterpret_cast<uint4*>(dst + off1 + 2048 * j) = first ? x : y;
+      }
+    };
+    locate();
+    load(rk, 0);
+    load_scales();
+    load(rv, 1);
+    float base = 0.f;
+    for (uint32_t n = 0, seg = 0; more; ++n) {
+      const int buf = n & 1;
+      bool ok = pt_wait(&bars[TB_KFREE + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (warp == 8) {  // scales of the step's four records (lanes 0-3)
+        const bool there = lane < 4 && sc.y == sc.y && sc.y > 0.f;
+        // log2 in two parts: exact for a power of two
+        const float lv = there ? (float)((int)(__float_as_uint(sc.y) >> 23) - 127) +
+                                     log2f(__uint_as_float((__float_as_uint(sc.y) & 0x7FFFFFu) | 0x3F800000u))
+                               : __uint_as_float(0x7FC00000u);
+        if (step == s.k0) {
+          const uint32_t m = __ballot_sync(0xffffffffu, there);
+          base = m ? __shfl_sync(0xffffffffu, lv, __ffs(m) - 1) : 0.f;
+          if (lane == 0) s_base[seg & 3] = base;
+        }
+        if (lane < 4) {
+          s_ks[4 * (n & 3) + lane] = sc.x;
+          s_lv[4 * (n & 3) + lane] = lv;
+          s_w[4 * (n & 3) + lane] = fast_exp2(base - lv);
+        }
+      }
+      expand(rk, smem + SM::k + 32768 * buf);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&bars[TB_KFULL + buf]);
+      // the next step's loads go out as the registers fall free
+      if (++step == s.k1) {
+        more = s.next(a);
+        step = s.k0;
+        ++seg;
+      }
+      if (more) {
+        locate();
+        load(rk, 0);
+        load_scales();
+      }
+      ok = pt_wait(&bars[TB_VFREE + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      expand(rv, smem + SM::v + 32768 * buf);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&bars[TB_VFULL + buf]);
+      if (more) load(rv, 1);
+    }
+  } else if (lane == 0) {
+    // ==== MMAs; first, where the blocks that start in this run are cut
+    {
+      auto cta_of = [&](long long y) {  // the last CTA whose run starts at or before step y
+        long long k = y * N / total;
+        while ((k + 1) * total / N <= y) ++k;
+        while (k * total / N > y) --k;
+        return (int)k;
+      };
+      PtWalk w = s;
+      do
+        if (w.k0 == 0)
+          a.cut[(size_t)w.e * Hkv + w.kvh] = make_int2(2 * c + (w.pos == lo ? 0 : 1), cta_of(w.pos + w.x.steps - 1));
+      while (w.next(a));
+    }
+    const uint32_t idS = umma_idesc_f16(128, PT_BN), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
+    const uint32_t qa = smem_addr(smem + SM::q), ka = smem_addr(smem + SM::k), va = smem_addr(smem + SM::v);
+    uint32_t n = 0, seg = 0, done[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int t, uint32_t step, bool last) {
+      const uint32_t q = qa + 32768 * t, k = ka + 32768 * (step & 1), d = tmem + PT_S_COL + 128 * t;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        umma_f16(d, umma_sdesc_sw128(q + (ks >> 2) * 16384 + (ks & 3) * 32),
+                 umma_sdesc_sw128(k + (ks >> 2) * 16384 + (ks & 3) * 32), idS, ks > 0);
+      umma_commit(&bars[TB_SFULL + t]);
+      if (last) umma_commit(&bars[TB_KFREE + (step & 1)]);
+    };
+    do {
+      const int tiles = s.x.n_live * G > PT_TILE ? 2 : 1, steps = s.k1 - s.k0;
+      ok = ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status);
+      ok = ok && pt_wait(&bars[TB_KFULL + (n & 1)], (n >> 1) & 1, abort, a.v.status);
+      if (!ok) break;
+      tc_fence_after();
+      for (int t = 0; t < tiles; ++t) scores(t, n, t == tiles - 1);
+      for (int i = 0; i < steps && ok; ++i, ++n) {
+        for (int t = 0; t < tiles; ++t) {
+          ok = ok && pt_wait(&bars[TB_PFULL + t], done[t]++ & 1, abort, a.v.status);
+          if (t == 0) ok = ok && pt_wait(&bars[TB_VFULL + (n & 1)], (n >> 1) & 1, abort, a.v.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t p = tmem + PT_S_COL + 128 * t, v = va + 32768 * (n & 1), d = tmem + PT_O_COL + 128 * t;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) umma_f16_ts(d, p + 8 * ks, umma_sdesc_sw128_mn(v + 2048 * ks, 128), idO, i > 0 || ks > 0);
+          umma_commit(&bars[TB_ODONE + t]);
+          if (t == tiles - 1) umma_commit(&bars[TB_VFREE + (n & 1)]);
+          if (i + 1 < steps) {
+            if (t == 0) ok = pt_wait(&bars[TB_KFULL + ((n + 1) & 1)], ((n + 1) >> 1) & 1, abort, a.v.status);
+            if (!ok) break;
+            tc_fence_after();
+            scores(t, n + 1, t == tiles - 1);
+          }
+        }
+      }
+      ++seg;
+    } while (ok && s.next(a));
+    umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released
+    mbar_wait(&bars[TB_DRAIN], 0, nullptr);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_free(tmem, 512);
+}
+
+// Merge of the blocks that were cut: a warp per row, its partials in order.
+static __global__ void __launch_bounds__(256) prefill8_merge_kernel(PtArgs a) {
+  pdl_wait();
+  const int Hkv = a.v.n_kv_heads, G = a.g_real;
+  const int e = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv;
+  const PtEntry x = pt_entry(a, e);
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= x.n_live * G) return;
+  const int2 cut = a.cut[blockIdx.x];
+  const int first = cut.x, c0 = first >> 1, c1 = cut.y;
+  if (c0 == c1) return;
+  auto row_of = [&](int k) { return (size_t)(k == c0 ? first : 2 * k) * PT_ROWS + r; };
+  float M = -CUDART_INF_F, MO = -CUDART_INF_F;
+  for (int k = c0; k <= c1; ++k) {
+    const float4 ml = a.part_ml[row_of(k)];
+    M = fmaxf(M, ml.x);
+    MO = fmaxf(MO, ml.y);
+  }
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = c0; k <= c1; ++k) {
+    const float4 ml = a.part_ml[row_of(k)];
+    if (ml.z == 0.f) continue;
+    const float4 y = reinterpret_cast<const float4*>(a.part_o + row_of(k) * D)[lane];
+    L += ml.z * fast_exp2(ml.x - M);
+    const float f = fast_exp2(ml.y - MO);
+    o.x = fmaf(y.x, f, o.x); o.y = fmaf(y.y, f, o.y); o.z = fmaf(y.z, f, o.z); o.w = fmaf(y.w, f, o.w);
+  }
+  const float f = L > 0.f ? fast_exp2(MO - M) / L : (L == L ? 0.f : L);
+  const size_t row = ((size_t)x.b * a.n_tok + x.tok0 + r / G) * a.n_q_heads + (size_t)kvh * G + r % G;
+  store4(a.out, a.dtype, row * D + 4 * lane, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
+}
+
+struct PtPlan {
+  int tq, n_blk, ctas;
+  size_t cut_bytes, bytes;
+};
+inline PtPlan pt_plan(int batch, int n_tok, int g, int n_kv_heads, int max_ctx) {
+  PtPlan p;
+  p.tq = PT_ROWS / g;
+  p.n_blk = (n_tok + p.tq - 1) / p.tq;
+  const long long steps = (long long)batch * p.n_blk * n_kv_heads * ((max_ctx + PT_BN - 1) / PT_BN);
+  p.ctas = (int)std::max(1ll, std::min((long long)sm_count(), steps));
+  p.cut_bytes = ((size_t)batch * p.n_blk * n_kv_heads * sizeof(int2) + 255) & ~(size_t)255;
+  p.bytes = p.cut_bytes + 2 * (size_t)p.ctas * PT_ROWS * (sizeof(float4) + D * sizeof(float));
+  return p;
+}
+
+inline int launch_prefill8_tc(const View8& v, const void* q, int dtype, int batch, int n_tok, int n_q_heads,
+                              const int32_t* start, const int32_t* n_valid, int max_ctx, float scale, void* out,
+                              void* workspace, void* stream) {
+  PtArgs a;
+  a.v = v;
+  a.q = q;
+  a.dtype = dtype;
+  a.batch = batch;
+  a.n_tok = n_tok;
+  a.n_q_heads = n_q_heads;
+  a.g_real = n_q_heads / v.n_kv_heads;
+  const PtPlan p = pt_plan(batch, n_tok, a.g_real, v.n_kv_heads, max_ctx);
+  a.tq = p.tq;
+  a.n_blk = p.n_blk;
+  a.max_ctx = max_ctx;
+  a.start = start;
+  a.n_valid = n_valid;
+  a.scale = scale;
+  a.out = out;
+  uint8_t* w = (uint8_t*)workspace;
+  a.cut = (int2*)w;
+  a.part_ml = (float4*)(w + p.cut_bytes);
+  a.part_o = (float*)(w + p.cut_bytes + 2 * (size_t)p.ctas * PT_ROWS * sizeof(float4));
+  auto fn = v.code == IQ_E4M3 ? prefill8_tc_kernel<IQ_E4M3> : prefill8_tc_kernel<IQ_S8>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PtSmem::bytes);
+  if (e != cudaSuccess) return (int)e;
+  e = launch_pdl(fn, dim3(p.ctas), dim3(PT_THREADS), PtSmem::bytes, (cudaStream_t)stream, a);
+  if (e != cudaSuccess || p.ctas == 1) return (int)e;
+  const int rows = std::min(n_tok, p.tq) * a.g_real;
+  return (int)launch_pdl(prefill8_merge_kernel, dim3((unsigned)(batch * p.n_blk * v.n_kv_heads), (rows + 7) / 8), dim3(256), 0,
+                         (cudaStream_t)stream, a);
+}
+
+}  // namespace iq

@@ -251,6 +251,24 @@ def test_decode_over_many_splits_and_many_sequences(batch, hkv, lens):
         _check_rows(o[b], q[b].double().numpy(), np.stack([x[0] for x in kv]), np.stack([x[1] for x in kv]), 0.05, F32)
 
 
+@pytest.mark.parametrize("lens", [[0, 0], [1, 0], [40, 700], [3, 260]])
+def test_lengths_far_below_the_bound(lens):
+    """max_ctx sizes the grid; the lengths decide what there is to share out."""
+    h = _filled(2, 1, 64, 200, "e4m3", lens, 42)
+    q = torch.randn((2, 4, 128), generator=torch.Generator().manual_seed(2)).to(F16)
+    o = _decode(h, q, lens, 12800)
+    for b, n in enumerate(lens):
+        k, v = h.kv(b, 0, n)
+        _check_rows(o[b], q[b].double().numpy(), k[None], v[None], 128 ** -0.5, F16)
+    assert h.c.status.item() == 0
+    for dtype in (F16, F32):
+        q = torch.randn((2, 3, 4, 128), generator=torch.Generator().manual_seed(2)).to(dtype)
+        start, cnt = [max(0, n - 3) for n in lens], [min(3, n) for n in lens]
+        o = _prefill(h, q, start, 12800, cnt)
+        _check_prefill(h, q, o, start, cnt, dtype)
+    assert h.c.status.item() == 0
+
+
 def test_decode_contiguous_cache_and_lengths_out_of_range():
     h = _filled(3, 2, 128, 1, "s8", [128, 60, 5], 40, contiguous=True)
     q = torch.randn((3, 2, 128), generator=torch.Generator().manual_seed(2)).to(BF16)
