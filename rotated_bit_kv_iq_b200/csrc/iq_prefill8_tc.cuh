@@ -15,7 +15,8 @@
 // Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that
 // neither causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block
 // cut by a run's end leaves partials, which a second kernel merges in order.
-// Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 the expansion, 12 issues the MMAs:
+// Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
+// issues the MMAs:
 // while one tile's scores are in the softmax, the tensor core works for the other tile.
 #pragma once
 #include <algorithm>
@@ -28,7 +29,10 @@ namespace iq {
 constexpr int PT_TILE = 128;  // rows of a tile: the MMA's M
 constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
-constexpr int PT_THREADS = 416;
+constexpr int PT_THREADS = 640;
+// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; what the block is launched with is 5 * 96
+constexpr int PT_REG_SOFTMAX = 144, PT_REG_EXPAND = 72, PT_REG_MMA = 48;
+static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
 constexpr float PT_SLACK = 8.f;
 
@@ -40,8 +44,8 @@ struct PtSmem {
   static constexpr int lv = ks + 64;          // float [4][4]: log2 of the V scales; NaN: the record is not there
   static constexpr int w = lv + 64;           // float [4][4]: 2^(base - log2 of the V scale)
   static constexpr int base = w + 64;         // float [4]: base of segment mod 4
-  static constexpr int scan = base + 16;      // int64 [13], then the plan: int [4]
-  static constexpr int bars = scan + 128;     // uint64 [TB_COUNT]
+  static constexpr int scan = base + 16;      // int64 [20], then the plan: int [4]
+  static constexpr int bars = scan + 192;     // uint64 [TB_COUNT]
   static constexpr int misc = bars + 20 * 8;  // uint32 tensor-memory base, int abort
   static constexpr int bytes = misc + 16 + 1024;
 };
@@ -54,7 +58,7 @@ enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_
 struct PtArgs {
   View8 v;
   const void* q;
-  int dtype, batch, n_tok, n_q_heads, g_real, tq, n_blk, max_ctx;
+  int dtype, batch, n_tok, n_q_heads, g_real, tq, n_blk, max_ctx, ctas;
   const int32_t* start;
   const int32_t* n_valid;
   float scale;
@@ -100,9 +104,9 @@ __device__ __forceinline__ PtEntry pt_entry(const PtArgs& a, int e) {
 // A CTA's run of (block, step) pairs, one segment (steps [k0, k1) of one block) after another.
 struct PtWalk {
   PtEntry x;
-  long long pos, end;
+  int pos, end;  // within the run
   int e, kvh, k0, k1;
-  __device__ __forceinline__ void cut() { k1 = (int)min((long long)x.steps, k0 + (end - pos)); }
+  __device__ __forceinline__ void cut() { k1 = min(x.steps, k0 + (end - pos)); }
   __device__ __forceinline__ bool next(const PtArgs& a) {  // false at the run's end
     pos += k1 - k0;
     if (pos >= end) return false;
@@ -117,6 +121,17 @@ struct PtWalk {
   }
 };
 
+// 16 bytes past L1, of which shared memory leaves little.
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+template <int REGS>
+__device__ __forceinline__ void set_registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void set_registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
 template <int CODE>
 __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   using SM = PtSmem;
@@ -126,7 +141,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::misc);
   volatile int* const abort = reinterpret_cast<volatile int*>(smem + SM::misc + 4);
   long long* const s_scan = reinterpret_cast<long long*>(smem + SM::scan);
-  int* const s_plan = reinterpret_cast<int*>(smem + SM::scan + 13 * 8);
+  int* const s_plan = reinterpret_cast<int*>(smem + SM::scan + 20 * 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
   if (tid == 0) {
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       if (cnt < 0 || cnt > a.n_tok || st < 0 || st > a.max_ctx - max(0, min(a.n_tok, cnt))) atomicOr(a.v.status, IQ_DEVERR_CTX);
     }
   if (lo >= hi) return;
-  if (warp == 12) tmem_alloc(tmem_slot, 512);
+  if (warp == 16) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -189,12 +204,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   s.x = pt_entry(a, s.e);
   s.kvh = s_plan[1] / s.x.steps;
   s.k0 = s_plan[1] % s.x.steps;
-  s.pos = lo;
-  s.end = hi;
+  s.pos = 0;
+  s.end = (int)(hi - lo);
   s.cut();
 
   if (warp < 8) {
     // ==== softmax: thread = row r of the block (row r mod 128 of tile t)
+    set_registers_up<PT_REG_SOFTMAX>();
     const int t = warp >> 2, r = 128 * t + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + PT_S_COL + 128 * t, tO = tmem + lanes + PT_O_COL + 128 * t;
@@ -253,6 +269,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           tc_fence_after();
           const int slot = 4 * ((n + i - s.k0) & 3);
           const int lim = qpos - PT_BN * i;  // keys 0 .. lim of the step
+          // the scores of two of the step's four records at a time: first the last two, for the maximum alone
+          uint32_t x[2][32];
+          tmem_ld32(tS + 64, x[0]);
+          tmem_ld32(tS + 96, x[1]);
           float f[4], lv[4];
           bool there = true;
 #pragma unroll
@@ -261,23 +281,33 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
             lv[b] = s_lv[slot + b];
             there = there && lv[b] == lv[b];
           }
-          const bool full = __all_sync(0xffffffffu, lim >= PT_BN - 1) && there;
-          float mo = -CUDART_INF_F;
+          // some key is not seen by some row of the warp, or some record is not there
+          const bool some = !there || __any_sync(0xffffffffu, lim < PT_BN - 1);
+          auto hide = [&](uint32_t (&y)[32], int b) {
+            const int last = lv[b] == lv[b] ? lim - 32 * b : -1;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            uint32_t x[32];
-            tmem_ld32(tS + 32 * b, x);
-            tmem_wait_ld();
+            for (int k = 0; k < 32; ++k) y[k] = k <= last ? y[k] : 0xFF800000u;
+          };
+          auto top = [&](const uint32_t (&y)[32], int b) {
             float mx = -CUDART_INF_F;
-            if (full) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(x[k]));
-            } else if (lv[b] == lv[b]) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, 32 * b + k <= lim ? __uint_as_float(x[k]) : -CUDART_INF_F);
-            }
-            if (mx > -CUDART_INF_F) mo = fmaxf(mo, fmaf(mx, f[b], lv[b]));
+            for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
+            return mx == -CUDART_INF_F ? mx : fmaf(mx, f[b], lv[b]);
+          };
+          tmem_wait_ld();
+          if (some) {
+            hide(x[0], 2);
+            hide(x[1], 3);
           }
+          float mo = fmaxf(top(x[0], 2), top(x[1], 3));
+          tmem_ld32(tS, x[0]);
+          tmem_ld32(tS + 32, x[1]);
+          tmem_wait_ld();
+          if (some) {
+            hide(x[0], 0);
+            hide(x[1], 1);
+          }
+          mo = fmaxf(mo, fmaxf(top(x[0], 0), top(x[1], 1)));
           if (i == s.k0) {
             ref = mo;
           } else {
@@ -289,49 +319,49 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
               if (up) ref = mo;
               l *= al;
-#pragma unroll
+#pragma unroll 1
               for (int b = 0; b < 8; ++b) {
-                uint32_t x[16];
-                tmem_ld16(tO + 16 * b, x);
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * b, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
-                tmem_st16(tO + 16 * b, x);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                tmem_st16(tO + 16 * b, o);
               }
             }
           }
           const float at = ref == -CUDART_INF_F ? 0.f : ref;
+          // probabilities, and P over the columns of S that are in registers or used up
+          auto weigh = [&](const uint32_t (&y)[32], int b) {
+            const bool here = lv[b] == lv[b];
+            const float add1 = here ? lv[b] - at : 0.f, f1 = here ? f[b] : 1.f;
+            const uint64_t ff = f2(f1, f1), add = f2(add1, add1);
+            uint64_t sum = 0;
+            uint32_t pp[16];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            uint32_t x[32], p[16];
-            tmem_ld32(tS + 32 * b, x);
-            tmem_wait_ld();
-            const float add = lv[b] - at;
-            float sum = 0.f;
-            if (full) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float p0 = fast_exp2(fmaf(__uint_as_float(x[k]), f[b], add));
-                const float p1 = fast_exp2(fmaf(__uint_as_float(x[k + 1]), f[b], add));
-                sum += p0 + p1;
-                p[k / 2] = half2_bits(p0, p1);
-              }
-              l = fmaf(sum, s_w[slot + b], l);
-            } else if (lv[b] == lv[b]) {
-#pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const float p0 = 32 * b + k <= lim ? fast_exp2(fmaf(__uint_as_float(x[k]), f[b], add)) : 0.f;
-                const float p1 = 32 * b + k + 1 <= lim ? fast_exp2(fmaf(__uint_as_float(x[k + 1]), f[b], add)) : 0.f;
-                sum += p0 + p1;
-                p[k / 2] = half2_bits(p0, p1);
-              }
-              l = fmaf(sum, s_w[slot + b], l);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) p[k] = 0u;
+            for (int k = 0; k < 32; k += 2) {
+              float y0, y1;
+              f2s(fma2(f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), ff, add), y0, y1);
+              y0 = fast_exp2(y0);
+              y1 = fast_exp2(y1);
+              sum = add2(sum, f2(y0, y1));
+              pp[k / 2] = half2_bits(y0, y1);
             }
-            tmem_st16(tS + 16 * b, p);  // P over the columns of S that are already used up
-          }
+            tmem_st16(tS + 16 * b, pp);
+            float s0, s1;
+            f2s(sum, s0, s1);
+            l = fmaf(s0 + s1, s_w[slot + b], l);
+          };
+          weigh(x[0], 0);
+          tmem_ld32(tS + 64, x[0]);
+          weigh(x[1], 1);
+          tmem_wait_ld();
+          tmem_ld32(tS + 96, x[1]);
+          if (some) hide(x[0], 2);
+          weigh(x[0], 2);
+          tmem_wait_ld();
+          if (some) hide(x[1], 3);
+          weigh(x[1], 3);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars[TB_PFULL + t]);
@@ -342,7 +372,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         const bool whole = s.k0 == 0 && s.k1 == s.x.steps;
         const float base = s_base[seg & 3];
         const float inv = l > 0.f ? fast_exp2(base) / l : (l == l ? 0.f : l);
-        const size_t prow = (size_t)(2 * c + (s.pos == lo ? 0 : 1)) * PT_ROWS + r;
+        const size_t prow = (size_t)(2 * c + (s.pos == 0 ? 0 : 1)) * PT_ROWS + r;
         if (!whole) a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f) : make_float4(ref - base, ref, l, 0.f);
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -365,159 +395,156 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       n += s.k1 - s.k0;
       ++seg;
     } while (s.next(a));
-  } else if (warp < 12) {
-    // ==== expansion: eight lanes to a 128-byte row of codes; keys 16 j + (e / 8), j = 0 .. 7
-    const int e = tid - 256, p8 = e & 7, r16 = e >> 3;
+  } else if (warp < 16) {
+    // ==== expansion: warps 8-11 K, 12-15 V; eight lanes to a 128-byte row of codes, 16 rows at a time, the codes of
+    // the next step on their way in registers while this one's buffer becomes free
+    set_registers_down<PT_REG_EXPAND>();
+    const int side = warp >= 12, e = tid & 127;
+    // eight lanes that store together take four chunks of a row and the same four of the next one: the rows'
+    // swizzles differ in their lowest bit, so that the eight never meet in a bank
+    const int p8 = (e & 3) | ((e >> 1) & 4), r16 = ((e >> 2) & 1) | ((e >> 3) & 14);
     const int ch = p8 ^ (r16 & 7);  // the 16 coordinates that this thread's 16 bytes hold
-    float* const s_ks = reinterpret_cast<float*>(smem + SM::ks);
-    float* const s_lv = reinterpret_cast<float*>(smem + SM::lv);
-    float* const s_w = reinterpret_cast<float*>(smem + SM::w);
-    float* const s_base = reinterpret_cast<float*>(smem + SM::base);
-    // the two binary16 chunks: the halves of the lanes start with different ones, so that eight lanes of a row
-    // never meet in a bank
-    const int first = (ch >> 2) & 1;
-    const uint32_t off0 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3) + first) ^ (r16 & 7)) << 4);
-    const uint32_t off1 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3) + 1 - first) ^ (r16 & 7)) << 4);
-    const uint8_t* rec[4];
-    uint4 rk[8], rv[8];
-    float2 sc = make_float2(0.f, 0.f);
-    int step = s.k0;
+    const uint32_t off0 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3)) ^ (r16 & 7)) << 4), off1 = off0 ^ 16;
+    const int from = side * TILE8_V + r16 * D + 16 * p8;
+    const int page_tiles = a.v.page_size / TILE_TOKENS;
+    struct Codes {
+      uint4 u[8];
+      float2 sc;  // K side, thread b < 4: scales of record b (V: NaN where it is not there)
+      bool first, valid;  // of a segment; at all
+    };
+    int step = s.k0, idx = 0, in_page = 0;
     bool more = true;
-    auto locate = [&]() {  // the records of the step
+    auto fetch = [&](Codes& z) {
+      z.valid = more;
+      if (!more) return;
+      z.first = step == s.k0;
+      // the page's place in the table and the tile's place in the page move on by one, and are found anew where a
+      // segment starts
+      if (z.first) {
+        idx = PT_BN / TILE_TOKENS * step / page_tiles;
+        in_page = PT_BN / TILE_TOKENS * step % page_tiles;
+      }
+      z.sc = make_float2(0.f, __uint_as_float(0x7FC00000u));
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int at = PT_BN * step + TILE_TOKENS * b;
-        rec[b] = nullptr;
-        if (at < s.x.kv_end) {
-          uint32_t err = 0;
-          const int page = find_page8(a.v, s.x.b, at, &err);
-          if (page >= 0) rec[b] = tile_record8(a.v, page, s.kvh, at % a.v.page_size);
-          else if (e == 0 && a.v.status) atomicOr(a.v.status, err);
+        const uint8_t* rec = nullptr;
+        if (PT_BN * step + TILE_TOKENS * b < s.x.kv_end) {
+          const int page = idx >= a.v.max_pages ? -1 : a.v.block_table ? a.v.block_table[(size_t)s.x.b * a.v.max_pages + idx] : s.x.b;
+          if (page >= 0 && page < a.v.n_pages)
+            rec = a.v.pool + (((size_t)page * Hkv + s.kvh) * page_tiles + in_page) * (size_t)TILE8_BYTES;
+          else if (e == 0 && a.v.status)
+            atomicOr(a.v.status, IQ_DEVERR_PAGE);
         }
+        if (++in_page == page_tiles) {
+          in_page = 0;
+          ++idx;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          z.u[2 * b + h] = make_uint4(0, 0, 0, 0);
+          if (rec && PT_BN * step + 32 * b + 16 * h + r16 < s.x.kv_end)
+            z.u[2 * b + h] = ld_stream(rec + from + 16 * D * h);
+        }
+        if (!side && e == b && rec) z.sc = *reinterpret_cast<const float2*>(rec + TILE8_SCALES);
+      }
+      if (++step == s.k1) {
+        more = s.next(a);
+        step = s.k0;
       }
     };
-    auto load = [&](uint4 (&u)[8], int side) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = 16 * j + r16;
-        u[j] = make_uint4(0, 0, 0, 0);
-        if (rec[j >> 1] && PT_BN * step + key < s.x.kv_end)
-          u[j] = __ldg(reinterpret_cast<const uint4*>(rec[j >> 1] + side * TILE8_V + (16 * (j & 1) + r16) * D + 16 * p8));
-      }
-    };
-    auto load_scales = [&]() {
-      sc = make_float2(0.f, __uint_as_float(0x7FC00000u));
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (e == b && rec[b]) sc = *reinterpret_cast<const float2*>(rec[b] + TILE8_SCALES);
-    };
-    auto expand = [&](const uint4 (&u)[8], uint8_t* dst) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint4 x, y;
-        codes4_to_half2x2<CODE>(u[j].x, x.x, x.y);
-        codes4_to_half2x2<CODE>(u[j].y, x.z, x.w);
-        codes4_to_half2x2<CODE>(u[j].z, y.x, y.y);
-        codes4_to_half2x2<CODE>(u[j].w, y.z, y.w);
-        *reinterpret_cast<uint4*>(dst + off0 + 2048 * j) = first ? y : x;
-        *reinterpret_cast<uint4*>(dst + off1 + 2048 * j) = first ? x : y;
-      }
-    };
-    locate();
-    load(rk, 0);
-    load_scales();
-    load(rv, 1);
+    uint32_t n = 0, seg = (uint32_t)-1;
     float base = 0.f;
-    for (uint32_t n = 0, seg = 0; more; ++n) {
+    auto put = [&](const Codes& z) {
       const int buf = n & 1;
-      bool ok = pt_wait(&bars[TB_KFREE + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      const bool ok = pt_wait(&bars[(side ? TB_VFREE : TB_KFREE) + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
+      if (!__all_sync(0xffffffffu, ok)) return false;
       if (warp == 8) {  // scales of the step's four records (lanes 0-3)
-        const bool there = lane < 4 && sc.y == sc.y && sc.y > 0.f;
+        float* const s_ks = reinterpret_cast<float*>(smem + SM::ks);
+        float* const s_lv = reinterpret_cast<float*>(smem + SM::lv);
+        float* const s_w = reinterpret_cast<float*>(smem + SM::w);
+        float* const s_base = reinterpret_cast<float*>(smem + SM::base);
+        const bool there = lane < 4 && z.sc.y == z.sc.y && z.sc.y > 0.f;
         // log2 in two parts: exact for a power of two
-        const float lv = there ? (float)((int)(__float_as_uint(sc.y) >> 23) - 127) +
-                                     log2f(__uint_as_float((__float_as_uint(sc.y) & 0x7FFFFFu) | 0x3F800000u))
+        const float lv = there ? (float)((int)(__float_as_uint(z.sc.y) >> 23) - 127) +
+                                     log2f(__uint_as_float((__float_as_uint(z.sc.y) & 0x7FFFFFu) | 0x3F800000u))
                                : __uint_as_float(0x7FC00000u);
-        if (step == s.k0) {
+        if (z.first) {
+          ++seg;
           const uint32_t m = __ballot_sync(0xffffffffu, there);
           base = m ? __shfl_sync(0xffffffffu, lv, __ffs(m) - 1) : 0.f;
           if (lane == 0) s_base[seg & 3] = base;
         }
         if (lane < 4) {
-          s_ks[4 * (n & 3) + lane] = sc.x;
+          s_ks[4 * (n & 3) + lane] = z.sc.x;
           s_lv[4 * (n & 3) + lane] = lv;
-          s_w[4 * (n & 3) + lane] = fast_exp2(base - lv);
+          s_w[4 * (n & 3) + lane] = there ? fast_exp2(base - lv) : 0.f;
         }
       }
-      expand(rk, smem + SM::k + 32768 * buf);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars[TB_KFULL + buf]);
-      // the next step's loads go out as the registers fall free
-      if (++step == s.k1) {
-        more = s.next(a);
-        step = s.k0;
-        ++seg;
+      uint8_t* const dst = smem + (side ? SM::v : SM::k) + 32768 * buf;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint4 x, y;
+        codes4_to_half2x2<CODE>(z.u[j].x, x.x, x.y);
+        codes4_to_half2x2<CODE>(z.u[j].y, x.z, x.w);
+        codes4_to_half2x2<CODE>(z.u[j].z, y.x, y.y);
+        codes4_to_half2x2<CODE>(z.u[j].w, y.z, y.w);
+        *reinterpret_cast<uint4*>(dst + off0 + 2048 * j) = x;
+        *reinterpret_cast<uint4*>(dst + off1 + 2048 * j) = y;
       }
-      if (more) {
-        locate();
-        load(rk, 0);
-        load_scales();
-      }
-      ok = pt_wait(&bars[TB_VFREE + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      expand(rv, smem + SM::v + 32768 * buf);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars[TB_VFULL + buf]);
-      if (more) load(rv, 1);
-    }
-  } else if (lane == 0) {
-    // ==== MMAs; first, where the blocks that start in this run are cut
-    {
-      auto cta_of = [&](long long y) {  // the last CTA whose run starts at or before step y
-        long long k = y * N / total;
-        while ((k + 1) * total / N <= y) ++k;
-        while (k * total / N > y) --k;
-        return (int)k;
-      };
-      PtWalk w = s;
-      do
-        if (w.k0 == 0)
-          a.cut[(size_t)w.e * Hkv + w.kvh] = make_int2(2 * c + (w.pos == lo ? 0 : 1), cta_of(w.pos + w.x.steps - 1));
-      while (w.next(a));
-    }
+      mbar_arrive(&bars[(side ? TB_VFULL : TB_KFULL) + buf]);
+      ++n;
+      return true;
+    };
+    Codes z;
+    for (fetch(z); z.valid; fetch(z))
+      if (!put(z)) break;
+  } else {
+    set_registers_down<PT_REG_MMA>();
+    if (warp == 16) {
+    // ==== MMAs: the warp waits together, one lane issues
     const uint32_t idS = umma_idesc_f16(128, PT_BN), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
-    const uint32_t qa = smem_addr(smem + SM::q), ka = smem_addr(smem + SM::k), va = smem_addr(smem + SM::v);
+    const uint64_t dq = umma_sdesc_sw128(smem_addr(smem + SM::q)), dk = umma_sdesc_sw128(smem_addr(smem + SM::k)),
+                   dv = umma_sdesc_sw128_mn(smem_addr(smem + SM::v), 128);
     uint32_t n = 0, seg = 0, done[2] = {0, 0};
     bool ok = true;
-    auto scores = [&](int t, uint32_t step, bool last) {
-      const uint32_t q = qa + 32768 * t, k = ka + 32768 * (step & 1), d = tmem + PT_S_COL + 128 * t;
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        umma_f16(d, umma_sdesc_sw128(q + (ks >> 2) * 16384 + (ks & 3) * 32),
-                 umma_sdesc_sw128(k + (ks >> 2) * 16384 + (ks & 3) * 32), idS, ks > 0);
-      umma_commit(&bars[TB_SFULL + t]);
-      if (last) umma_commit(&bars[TB_KFREE + (step & 1)]);
+    auto wait = [&](int bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[bar], parity & 1, abort, a.v.status));
+    };
+    auto scores = [&](int t, uint32_t step, bool last) {  // 32 KB (2048 descriptor units) to a tile, to a buffer
+      if (elect_one()) {
+        umma_f16_k128(tmem + PT_S_COL + 128 * t, dq + 2048 * t, dk + 2048 * (step & 1), idS);
+        umma_commit(&bars[TB_SFULL + t]);
+        if (last) umma_commit(&bars[TB_KFREE + (step & 1)]);
+      }
+      __syncwarp();
     };
     do {
       const int tiles = s.x.n_live * G > PT_TILE ? 2 : 1, steps = s.k1 - s.k0;
-      ok = ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status);
-      ok = ok && pt_wait(&bars[TB_KFULL + (n & 1)], (n >> 1) & 1, abort, a.v.status);
+      if (lane == 0) {  // where the block is cut, for the merge
+        int2* const cut = a.cut + (size_t)s.e * Hkv + s.kvh;
+        if (s.k0 == 0) cut->x = 2 * c + (s.pos == 0 ? 0 : 1);
+        if (s.k1 == s.x.steps) cut->y = c;
+      }
+      wait(TB_Q, seg);
+      wait(TB_KFULL + (n & 1), n >> 1);
       if (!ok) break;
       tc_fence_after();
       for (int t = 0; t < tiles; ++t) scores(t, n, t == tiles - 1);
       for (int i = 0; i < steps && ok; ++i, ++n) {
         for (int t = 0; t < tiles; ++t) {
-          ok = ok && pt_wait(&bars[TB_PFULL + t], done[t]++ & 1, abort, a.v.status);
-          if (t == 0) ok = ok && pt_wait(&bars[TB_VFULL + (n & 1)], (n >> 1) & 1, abort, a.v.status);
+          if (t == 0) wait(TB_VFULL + (n & 1), n >> 1);
+          wait(TB_PFULL + t, done[t]++);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t p = tmem + PT_S_COL + 128 * t, v = va + 32768 * (n & 1), d = tmem + PT_O_COL + 128 * t;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) umma_f16_ts(d, p + 8 * ks, umma_sdesc_sw128_mn(v + 2048 * ks, 128), idO, i > 0 || ks > 0);
-          umma_commit(&bars[TB_ODONE + t]);
-          if (t == tiles - 1) umma_commit(&bars[TB_VFREE + (n & 1)]);
+          if (elect_one()) {
+            umma_f16_ts_k128(tmem + PT_O_COL + 128 * t, tmem + PT_S_COL + 128 * t, dv + 2048 * (n & 1), idO, i > 0);
+            umma_commit(&bars[TB_ODONE + t]);
+            if (t == tiles - 1) umma_commit(&bars[TB_VFREE + (n & 1)]);
+          }
+          __syncwarp();
           if (i + 1 < steps) {
-            if (t == 0) ok = pt_wait(&bars[TB_KFULL + ((n + 1) & 1)], ((n + 1) >> 1) & 1, abort, a.v.status);
+            if (t == 0) wait(TB_KFULL + ((n + 1) & 1), (n + 1) >> 1);
             if (!ok) break;
             tc_fence_after();
             scores(t, n + 1, t == tiles - 1);
@@ -526,13 +553,15 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       }
       ++seg;
     } while (ok && s.next(a));
-    umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released
+    if (elect_one()) umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released
+    __syncwarp();
     mbar_wait(&bars[TB_DRAIN], 0, nullptr);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 16) tmem_free(tmem, 512);
 }
 
 // Merge of the blocks that were cut: a warp per row, its partials in order.
@@ -544,7 +573,8 @@ static __global__ void __launch_bounds__(256) prefill8_merge_kernel(PtArgs a) {
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (r >= x.n_live * G) return;
   const int2 cut = a.cut[blockIdx.x];
-  const int first = cut.x, c0 = first >> 1, c1 = cut.y;
+  // (clamped: after a timeout they may not have been written)
+  const int first = max(0, min(2 * a.ctas - 1, cut.x)), c0 = first >> 1, c1 = max(c0, min(a.ctas - 1, cut.y));
   if (c0 == c1) return;
   auto row_of = [&](int k) { return (size_t)(k == c0 ? first : 2 * k) * PT_ROWS + r; };
   float M = -CUDART_INF_F, MO = -CUDART_INF_F;
@@ -597,6 +627,7 @@ inline int launch_prefill8_tc(const View8& v, const void* q, int dtype, int batc
   const PtPlan p = pt_plan(batch, n_tok, a.g_real, v.n_kv_heads, max_ctx);
   a.tq = p.tq;
   a.n_blk = p.n_blk;
+  a.ctas = p.ctas;
   a.max_ctx = max_ctx;
   a.start = start;
   a.n_valid = n_valid;

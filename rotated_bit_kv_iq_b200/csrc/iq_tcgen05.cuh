@@ -51,14 +51,37 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// The same with A (M lanes x 16 binary16 numbers, two to a 32-bit column) in tensor memory.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t acc) {
+// Eight MMAs over K = 128 from operands in the layouts above, R = 128 rows: the descriptors of the first one, and
+// for the rest the constant steps of their start addresses (in 16-byte units), so that one thread issues them back to
+// back.  A and B along K (two blocks of 64): steps 2, 4, 6, 1024, 1026, ...; D is overwritten.
+__device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+#define IQ_UMMA_STEP(off) "add.u64 a, %1, " #off ";\n add.u64 b, %2, " #off ";\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n "
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred f, t;\n .reg .b64 a, b;\n setp.ne.b32 f, 0, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n " IQ_UMMA_STEP(2) IQ_UMMA_STEP(4) IQ_UMMA_STEP(6)
+      IQ_UMMA_STEP(1024) IQ_UMMA_STEP(1026) IQ_UMMA_STEP(1028) IQ_UMMA_STEP(1030) "}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
+#undef IQ_UMMA_STEP
+}
+// The same with A (M lanes x 128 binary16 numbers, two to a 32-bit column: eight columns a step) in tensor memory and
+// B along N (2048 bytes a step); D is added to where acc != 0.
+__device__ __forceinline__ void umma_f16_ts_k128(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t acc) {
+#define IQ_UMMA_STEP(i) "add.u32 a, %1, 8 * " #i ";\n add.u64 b, %2, 128 * " #i ";\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n "
+  asm volatile(
+      "{\n .reg .pred p, t;\n .reg .b32 a;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n " IQ_UMMA_STEP(1) IQ_UMMA_STEP(2) IQ_UMMA_STEP(3)
+      IQ_UMMA_STEP(4) IQ_UMMA_STEP(5) IQ_UMMA_STEP(6) IQ_UMMA_STEP(7) "}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
       : "memory");
+#undef IQ_UMMA_STEP
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // The mbarrier receives one arrival once every MMA this thread has issued so far is complete.
