@@ -16,7 +16,7 @@
 // neither causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block
 // cut by a run's end leaves partials, which a second kernel merges in order.
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
-// issues the MMAs:
+// issues the MMAs, 17 finds the records:
 // while one tile's scores are in the softmax, the tensor core works for the other tile.
 #pragma once
 #include <algorithm>
@@ -30,8 +30,8 @@ constexpr int PT_TILE = 128;  // rows of a tile: the MMA's M
 constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
 constexpr int PT_THREADS = 640;
-// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; what the block is launched with is 5 * 96
-constexpr int PT_REG_SOFTMAX = 144, PT_REG_EXPAND = 72, PT_REG_MMA = 48;
+// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96
+constexpr int PT_REG_SOFTMAX = 136, PT_REG_EXPAND = 72, PT_REG_MMA = 64;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
 constexpr float PT_SLACK = 8.f;
@@ -40,20 +40,24 @@ struct PtSmem {
   static constexpr int q = 0;                 // [tile] 128 rows x 128 coordinates
   static constexpr int k = 65536;             // [buffer] 128 keys x 128 coordinates
   static constexpr int v = 131072;            // [buffer]
-  static constexpr int ks = 196608;           // float [4][4]: K scales of step n mod 4's tile records
-  static constexpr int lv = ks + 64;          // float [4][4]: log2 of the V scales; NaN: the record is not there
-  static constexpr int w = lv + 64;           // float [4][4]: 2^(base - log2 of the V scale)
-  static constexpr int base = w + 64;         // float [4]: base of segment mod 4
-  static constexpr int scan = base + 16;      // int64 [20], then the plan: int [4]
+  static constexpr int ks = 196608;           // float [8][4]: K scales of step n mod 8's records
+  static constexpr int lv = ks + 128;         // float [8][4]: log2 of the V scales; NaN: the record is not there
+  static constexpr int w = lv + 128;          // float [8][4]: 2^(base - log2 of the V scale)
+  static constexpr int base = w + 128;        // float [8]: the segment's base, log2 of its first V scale
+  static constexpr int rec = base + 32;       // int [4][4]: step n mod 4's records in the layer; -1: not there
+  static constexpr int keys = rec + 64;       // int [4]: the step's keys up to the block's last; 0: the run's end
+  static constexpr int scan = keys + 16;      // int64 [20], then the plan: int [4]
   static constexpr int bars = scan + 192;     // uint64 [TB_COUNT]
-  static constexpr int misc = bars + 20 * 8;  // uint32 tensor-memory base, int abort
+  static constexpr int misc = bars + 30 * 8;  // uint32 tensor-memory base, int abort
   static constexpr int bytes = misc + 16 + 1024;
 };
 static_assert(PtSmem::bytes <= 232448, "one CTA's shared memory");
 
-// mbarriers: K and V of step parity expanded / free again; per tile: scores ready, P written, O += P V done; queries.
-enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 10, TB_ODONE = 12, TB_Q = 14,
-       TB_DRAIN = 15, TB_COUNT = 16 };
+// mbarriers: K and V of step parity expanded / free again; by tile and half-step parity (2 t + b): scores ready, P
+// written, O += P V done (a barrier for each parity: a wait for half-step j knows of j - 2 at the least, so that the
+// phase's parity tells it from the one before); queries; records of step n mod 4 located / taken.
+enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 12, TB_ODONE = 16, TB_Q = 20,
+       TB_DRAIN = 21, TB_LFULL = 22, TB_LFREE = 26, TB_COUNT = 30 };
 
 struct PtArgs {
   View8 v;
@@ -146,10 +150,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
   if (tid == 0) {
     for (int i = 0; i < TB_COUNT; ++i) {
-      const int count = (i >= TB_KFULL && i < TB_KFULL + 2) || (i >= TB_VFULL && i < TB_VFULL + 2) ? 128
-                        : i >= TB_PFULL && i < TB_PFULL + 2                                        ? 128
-                        : i == TB_Q                                                                ? 256
-                                                                                                   : 1;
+      // one arrival a warp (of all 32 lanes' it would be 32 in a row)
+      const bool expanded = i == TB_KFULL || i == TB_KFULL + 1 || i == TB_VFULL || i == TB_VFULL + 1;
+      const bool written = i >= TB_PFULL && i < TB_PFULL + 4;
+      const int count = expanded || written ? 4 : i >= TB_LFREE || i == TB_Q ? 8 : 1;
       mbar_init(&bars[i], count);
     }
     mbar_fence_init();
@@ -209,16 +213,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   s.cut();
 
   if (warp < 8) {
-    // ==== softmax: thread = row r of the block (row r mod 128 of tile t)
+    // ==== softmax: thread = row r of the block (row r mod 128 of tile t); half-steps of 64 keys
     set_registers_up<PT_REG_SOFTMAX>();
     const int t = warp >> 2, r = 128 * t + 32 * (warp & 3) + lane;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = tmem + lanes + PT_S_COL + 128 * t, tO = tmem + lanes + PT_O_COL + 128 * t;
-    const float* const s_ks = reinterpret_cast<const float*>(smem + SM::ks);
-    const float* const s_lv = reinterpret_cast<const float*>(smem + SM::lv);
-    const float* const s_w = reinterpret_cast<const float*>(smem + SM::w);
-    const float* const s_base = reinterpret_cast<const float*>(smem + SM::base);
-    uint32_t done = 0;  // steps of this tile so far
+    uint32_t done = 0;  // half-steps of this tile so far
     uint32_t n = 0;     // steps of the run so far
     uint32_t seg = 0;
     bool ok = true;
@@ -232,14 +232,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         uint4 u[16];
         float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 16; ++i)
           u[i] = live ? __ldg(reinterpret_cast<const uint4*>((const uint16_t*)a.q + row * D) + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        auto widen = [&](uint32_t x) {
+          return a.dtype == IQ_F16 ? half2_floats(x) : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+        };
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = a.dtype == IQ_F16 ? half2_floats(x[j]) : make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+        for (int i = 0; i < 16; ++i) {
+          const float2 f0 = widen(u[i].x), f1 = widen(u[i].y), f2 = widen(u[i].z), f3 = widen(u[i].w);
+          amax = fmaxf(amax, fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                                   fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
         }
         int ex = (int)(__float_as_uint(amax) >> 23) - 127;
         ex = max(-100, min(126, ex));
@@ -247,157 +249,148 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         if (live) qs = a.scale * kLog2E8 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = a.dtype == IQ_F16 ? half2_floats(x[j]) : make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-            x[j] = half2_bits(f.x * sig, f.y * sig);
-          }
+          const float2 f0 = widen(u[i].x), f1 = widen(u[i].y), f2 = widen(u[i].z), f3 = widen(u[i].w);
           *reinterpret_cast<uint4*>(smem + SM::q + 32768 * t + umma_sw128_off(r & 127, 8 * i, PT_TILE)) =
-              make_uint4(x[0], x[1], x[2], x[3]);
+              make_uint4(half2_bits(f0.x * sig, f0.y * sig), half2_bits(f1.x * sig, f1.y * sig),
+                         half2_bits(f2.x * sig, f2.y * sig), half2_bits(f3.x * sig, f3.y * sig));
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars[TB_Q]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[TB_Q]);
       float ref = -CUDART_INF_F, l = 0.f;
       if (t < tiles) {
         const int qpos = live ? s.x.pos0 + tok : -1;  // the last key that the row sees
-        for (int i = s.k0; i < s.k1; ++i, ++done) {
-          ok = ok && pt_wait(&bars[TB_SFULL + t], done & 1, abort, a.v.status);
-          ok = __all_sync(0xffffffffu, ok);
+        const int halves = 2 * (s.k1 - s.k0);
+        for (int i = 0; i < halves; ++i, ++done) {
+          const int buf = done & 1;
+          ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + 2 * t + buf], (done >> 1) & 1, abort, a.v.status));
           if (!ok) break;
           tc_fence_after();
-          const int slot = 4 * ((n + i - s.k0) & 3);
-          const int lim = qpos - PT_BN * i;  // keys 0 .. lim of the step
-          // the scores of two of the step's four records at a time: first the last two, for the maximum alone
-          uint32_t x[2][32];
-          tmem_ld32(tS + 64, x[0]);
-          tmem_ld32(tS + 96, x[1]);
-          float f[4], lv[4];
-          bool there = true;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            f[b] = s_ks[slot + b] * qs;
-            lv[b] = s_lv[slot + b];
-            there = there && lv[b] == lv[b];
-          }
+          const int slot = 2 * ((n + (i >> 1)) & 7) + (i & 1);
+          const int lim = qpos - PT_BN * s.k0 - 64 * i;  // keys 0 .. lim of the half-step
+          const float2 ks = reinterpret_cast<const float2*>(smem + SM::ks)[slot];
+          const float2 lvs = reinterpret_cast<const float2*>(smem + SM::lv)[slot];
+          const float2 ws = reinterpret_cast<const float2*>(smem + SM::w)[slot];
           // some key is not seen by some row of the warp, or some record is not there
-          const bool some = !there || __any_sync(0xffffffffu, lim < PT_BN - 1);
-          auto hide = [&](uint32_t (&y)[32], int b) {
-            const int last = lv[b] == lv[b] ? lim - 32 * b : -1;
+          const bool some = __any_sync(0xffffffffu, lim < 63) || !(lvs.x == lvs.x) || !(lvs.y == lvs.y);
+          // One pass: the scores of a record, their maximum, and p' under the ref that stands.  P waits in registers
+          // until the maximum of the half-step is known; where it has passed ref by more than the slack (a block's
+          // first half-step, and rarely after it) the pass is made again under the new ref.
+          uint32_t pp[32];
+          float add_l;
+          auto pass = [&](float at) {
+            float mo = -CUDART_INF_F;
+            add_l = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = k <= last ? y[k] : 0xFF800000u;
-          };
-          auto top = [&](const uint32_t (&y)[32], int b) {
-            float mx = -CUDART_INF_F;
+            for (int b = 0; b < 2; ++b) {
+              uint32_t x[32];
+              tmem_ld32(tS + 64 * buf + 32 * b, x);
+              const float lv = b ? lvs.y : lvs.x;
+              const bool here = lv == lv;
+              const float f1 = here ? (b ? ks.y : ks.x) * qs : 1.f, add1 = here ? lv - at : 0.f;
+              const uint64_t ff = f2(f1, f1), add = f2(add1, add1);
+              tmem_wait_ld(x);
+              if (some) {
+                const int last = here ? lim - 32 * b : -1;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
-            return mx == -CUDART_INF_F ? mx : fmaf(mx, f[b], lv[b]);
+                for (int k = 0; k < 32; ++k) x[k] = k <= last ? x[k] : 0xFF800000u;
+              }
+              float mx[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
+#pragma unroll
+              for (int k = 4; k < 28; k += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(x[k + j]), __uint_as_float(x[k + j + 4])));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(x[28 + j]));
+              const float m1 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              if (m1 > -CUDART_INF_F) mo = fmaxf(mo, fmaf(m1, f1, here ? lv : 0.f));
+              uint64_t sum[2] = {0, 0};
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float y0, y1;
+                f2s(fma2(f2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff, add), y0, y1);
+                y0 = fast_exp2(y0);
+                y1 = fast_exp2(y1);
+                sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], f2(y0, y1));
+                pp[16 * b + k / 2] = half2_bits(y0, y1);
+              }
+              float s0, s1;
+              f2s(add2(sum[0], sum[1]), s0, s1);
+              add_l = fmaf(s0 + s1, b ? ws.y : ws.x, add_l);
+            }
+            return mo;
           };
-          tmem_wait_ld();
-          if (some) {
-            hide(x[0], 2);
-            hide(x[1], 3);
-          }
-          float mo = fmaxf(top(x[0], 2), top(x[1], 3));
-          tmem_ld32(tS, x[0]);
-          tmem_ld32(tS + 32, x[1]);
-          tmem_wait_ld();
-          if (some) {
-            hide(x[0], 0);
-            hide(x[1], 1);
-          }
-          mo = fmaxf(mo, fmaxf(top(x[0], 0), top(x[1], 1)));
-          if (i == s.k0) {
-            ref = mo;
-          } else {
-            const bool up = mo > ref + PT_SLACK;
-            if (__any_sync(0xffffffffu, up)) {
-              ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + t], (done - 1) & 1, abort, a.v.status));
+          const float mo = pass(ref == -CUDART_INF_F ? 0.f : ref);
+          const bool up = i == 0 || mo > ref + PT_SLACK;
+          if (__any_sync(0xffffffffu, up)) {
+            const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
+            if (up) ref = mo;
+            if (i > 0) {
+              ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + 2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort, a.v.status));
               if (!ok) break;
               tc_fence_after();
-              const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
-              if (up) ref = mo;
               l *= al;
 #pragma unroll 1
               for (int b = 0; b < 8; ++b) {
                 uint32_t o[16];
                 tmem_ld16(tO + 16 * b, o);
-                tmem_wait_ld();
+                tmem_wait_ld(o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
                 tmem_st16(tO + 16 * b, o);
               }
             }
+            pass(ref == -CUDART_INF_F ? 0.f : ref);
           }
-          const float at = ref == -CUDART_INF_F ? 0.f : ref;
-          // probabilities, and P over the columns of S that are in registers or used up
-          auto weigh = [&](const uint32_t (&y)[32], int b) {
-            const bool here = lv[b] == lv[b];
-            const float add1 = here ? lv[b] - at : 0.f, f1 = here ? f[b] : 1.f;
-            const uint64_t ff = f2(f1, f1), add = f2(add1, add1);
-            uint64_t sum = 0;
-            uint32_t pp[16];
+          l += add_l;
+          // P over the columns of S
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float y0, y1;
-              f2s(fma2(f2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), ff, add), y0, y1);
-              y0 = fast_exp2(y0);
-              y1 = fast_exp2(y1);
-              sum = add2(sum, f2(y0, y1));
-              pp[k / 2] = half2_bits(y0, y1);
-            }
-            tmem_st16(tS + 16 * b, pp);
-            float s0, s1;
-            f2s(sum, s0, s1);
-            l = fmaf(s0 + s1, s_w[slot + b], l);
-          };
-          weigh(x[0], 0);
-          tmem_ld32(tS + 64, x[0]);
-          weigh(x[1], 1);
-          tmem_wait_ld();
-          tmem_ld32(tS + 96, x[1]);
-          if (some) hide(x[0], 2);
-          weigh(x[0], 2);
-          tmem_wait_ld();
-          if (some) hide(x[1], 3);
-          weigh(x[1], 3);
+          for (int b = 0; b < 2; ++b)
+            tmem_st16(tS + 64 * buf + 16 * b, *reinterpret_cast<const uint32_t(*)[16]>(pp + 16 * b));
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&bars[TB_PFULL + t]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[TB_PFULL + 2 * t + buf]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + t], (done - 1) & 1, abort, a.v.status));
+        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + 2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort, a.v.status));
         if (!ok) break;
         tc_fence_after();
         const bool whole = s.k0 == 0 && s.k1 == s.x.steps;
-        const float base = s_base[seg & 3];
+        const float base = reinterpret_cast<const float*>(smem + SM::base)[(n + s.k1 - s.k0 - 1) & 7];
         const float inv = l > 0.f ? fast_exp2(base) / l : (l == l ? 0.f : l);
         const size_t prow = (size_t)(2 * c + (s.pos == 0 ? 0 : 1)) * PT_ROWS + r;
-        if (!whole) a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f) : make_float4(ref - base, ref, l, 0.f);
-#pragma unroll
+        if (!whole)
+          a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f) : make_float4(ref - base, ref, l, 0.f);
+#pragma unroll 1
         for (int b = 0; b < 8; ++b) {
           uint32_t x[16];
+          __syncwarp();
           tmem_ld16(tO + 16 * b, x);
-          tmem_wait_ld();
-          if (!live) continue;
+          tmem_wait_ld(x);
+          if (live) {
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
-            if (whole) store4(a.out, a.dtype, row * D + 16 * b + k, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-            else *reinterpret_cast<float4*>(a.part_o + prow * D + 16 * b + k) = y;
+            for (int k = 0; k < 16; k += 4) {
+              const float4 y = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+              if (whole) store4(a.out, a.dtype, row * D + 16 * b + k, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+              else *reinterpret_cast<float4*>(a.part_o + prow * D + 16 * b + k) = y;
+            }
           }
         }
+        __syncwarp();
         tc_fence_before();
       } else {  // no row of this tile: not ahead of the tile that has rows
-        ok = ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status));
+        if (!ok) break;
       }
       n += s.k1 - s.k0;
       ++seg;
     } while (s.next(a));
   } else if (warp < 16) {
-    // ==== expansion: warps 8-11 K, 12-15 V; eight lanes to a 128-byte row of codes, 16 rows at a time, the codes of
-    // the next step on their way in registers while this one's buffer becomes free
+    // ==== expansion: warps 8-11 K, 12-15 V; eight lanes to a 128-byte row of codes, 16 rows at a time.  The codes of
+    // the next step are loaded as this one's leave the registers.
     set_registers_down<PT_REG_EXPAND>();
     const int side = warp >= 12, e = tid & 127;
     // eight lanes that store together take four chunks of a row and the same four of the next one: the rows'
@@ -405,105 +398,116 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
     const int p8 = (e & 3) | ((e >> 1) & 4), r16 = ((e >> 2) & 1) | ((e >> 3) & 14);
     const int ch = p8 ^ (r16 & 7);  // the 16 coordinates that this thread's 16 bytes hold
     const uint32_t off0 = (uint32_t)(ch >> 2) * 16384 + r16 * 128 + (((2 * (ch & 3)) ^ (r16 & 7)) << 4), off1 = off0 ^ 16;
-    const int from = side * TILE8_V + r16 * D + 16 * p8;
-    const int page_tiles = a.v.page_size / TILE_TOKENS;
-    struct Codes {
-      uint4 u[8];
-      float2 sc;  // K side, thread b < 4: scales of record b (V: NaN where it is not there)
-      bool first, valid;  // of a segment; at all
+    const uint8_t* const codes = a.v.pool + side * TILE8_V + r16 * D + 16 * p8;
+    uint8_t* const tiles = smem + (side ? SM::v : SM::k);
+    uint64_t* const full = &bars[side ? TB_VFULL : TB_KFULL];
+    uint64_t* const freed = &bars[side ? TB_VFREE : TB_KFREE];
+    uint4 u[8];
+    int4 rec;
+    int keys;
+    bool ok = true;
+    auto where = [&](uint32_t m) {  // step m's records
+      ok = ok && pt_wait(&bars[TB_LFULL + (m & 3)], (m >> 2) & 1, abort, a.v.status);
+      ok = __all_sync(0xffffffffu, ok);
+      rec = reinterpret_cast<const int4*>(smem + SM::rec)[m & 3];
+      keys = ok ? reinterpret_cast<const int*>(smem + SM::keys)[m & 3] : 0;
     };
-    int step = s.k0, idx = 0, in_page = 0;
-    bool more = true;
-    auto fetch = [&](Codes& z) {
-      z.valid = more;
-      if (!more) return;
-      z.first = step == s.k0;
-      // the page's place in the table and the tile's place in the page move on by one, and are found anew where a
-      // segment starts
-      if (z.first) {
-        idx = PT_BN / TILE_TOKENS * step / page_tiles;
-        in_page = PT_BN / TILE_TOKENS * step % page_tiles;
-      }
-      z.sc = make_float2(0.f, __uint_as_float(0x7FC00000u));
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint8_t* rec = nullptr;
-        if (PT_BN * step + TILE_TOKENS * b < s.x.kv_end) {
-          const int page = idx >= a.v.max_pages ? -1 : a.v.block_table ? a.v.block_table[(size_t)s.x.b * a.v.max_pages + idx] : s.x.b;
-          if (page >= 0 && page < a.v.n_pages)
-            rec = a.v.pool + (((size_t)page * Hkv + s.kvh) * page_tiles + in_page) * (size_t)TILE8_BYTES;
-          else if (e == 0 && a.v.status)
-            atomicOr(a.v.status, IQ_DEVERR_PAGE);
-        }
-        if (++in_page == page_tiles) {
-          in_page = 0;
-          ++idx;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          z.u[2 * b + h] = make_uint4(0, 0, 0, 0);
-          if (rec && PT_BN * step + 32 * b + 16 * h + r16 < s.x.kv_end)
-            z.u[2 * b + h] = ld_stream(rec + from + 16 * D * h);
-        }
-        if (!side && e == b && rec) z.sc = *reinterpret_cast<const float2*>(rec + TILE8_SCALES);
-      }
-      if (++step == s.k1) {
-        more = s.next(a);
-        step = s.k0;
-      }
+    auto load = [&](int j) {
+      const int r = j < 2 ? rec.x : j < 4 ? rec.y : j < 6 ? rec.z : rec.w;
+      u[j] = make_uint4(0, 0, 0, 0);
+      if (r >= 0 && 16 * j + r16 < keys) u[j] = ld_stream(codes + (size_t)r * TILE8_BYTES + 16 * D * (j & 1));
     };
-    uint32_t n = 0, seg = (uint32_t)-1;
-    float base = 0.f;
-    auto put = [&](const Codes& z) {
-      const int buf = n & 1;
-      const bool ok = pt_wait(&bars[(side ? TB_VFREE : TB_KFREE) + buf], ((n >> 1) & 1) ^ 1, abort, a.v.status);
-      if (!__all_sync(0xffffffffu, ok)) return false;
-      if (warp == 8) {  // scales of the step's four records (lanes 0-3)
-        float* const s_ks = reinterpret_cast<float*>(smem + SM::ks);
-        float* const s_lv = reinterpret_cast<float*>(smem + SM::lv);
-        float* const s_w = reinterpret_cast<float*>(smem + SM::w);
-        float* const s_base = reinterpret_cast<float*>(smem + SM::base);
-        const bool there = lane < 4 && z.sc.y == z.sc.y && z.sc.y > 0.f;
-        // log2 in two parts: exact for a power of two
-        const float lv = there ? (float)((int)(__float_as_uint(z.sc.y) >> 23) - 127) +
-                                     log2f(__uint_as_float((__float_as_uint(z.sc.y) & 0x7FFFFFu) | 0x3F800000u))
-                               : __uint_as_float(0x7FC00000u);
-        if (z.first) {
-          ++seg;
-          const uint32_t m = __ballot_sync(0xffffffffu, there);
-          base = m ? __shfl_sync(0xffffffffu, lv, __ffs(m) - 1) : 0.f;
-          if (lane == 0) s_base[seg & 3] = base;
-        }
-        if (lane < 4) {
-          s_ks[4 * (n & 3) + lane] = z.sc.x;
-          s_lv[4 * (n & 3) + lane] = lv;
-          s_w[4 * (n & 3) + lane] = there ? fast_exp2(base - lv) : 0.f;
-        }
-      }
-      uint8_t* const dst = smem + (side ? SM::v : SM::k) + 32768 * buf;
+    where(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) load(j);
+    if (lane == 0) mbar_arrive(&bars[TB_LFREE]);
+    for (uint32_t n = 0; ok && keys; ++n) {
+      where(n + 1);
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, pt_wait(&freed[n & 1], ((n >> 1) & 1) ^ 1, abort, a.v.status));
+      if (!ok) break;
+      uint8_t* const dst = tiles + 32768 * (n & 1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint4 x, y;
-        codes4_to_half2x2<CODE>(z.u[j].x, x.x, x.y);
-        codes4_to_half2x2<CODE>(z.u[j].y, x.z, x.w);
-        codes4_to_half2x2<CODE>(z.u[j].z, y.x, y.y);
-        codes4_to_half2x2<CODE>(z.u[j].w, y.z, y.w);
+        codes4_to_half2x2<CODE>(u[j].x, x.x, x.y);
+        codes4_to_half2x2<CODE>(u[j].y, x.z, x.w);
+        codes4_to_half2x2<CODE>(u[j].z, y.x, y.y);
+        codes4_to_half2x2<CODE>(u[j].w, y.z, y.w);
+        load(j);
         *reinterpret_cast<uint4*>(dst + off0 + 2048 * j) = x;
         *reinterpret_cast<uint4*>(dst + off1 + 2048 * j) = y;
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&bars[(side ? TB_VFULL : TB_KFULL) + buf]);
-      ++n;
-      return true;
-    };
-    Codes z;
-    for (fetch(z); z.valid; fetch(z))
-      if (!put(z)) break;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&full[n & 1]);
+        mbar_arrive(&bars[TB_LFREE + ((n + 1) & 3)]);
+      }
+    }
   } else {
     set_registers_down<PT_REG_MMA>();
-    if (warp == 16) {
+    if (warp == 17) {
+      // ==== where the records of each step are, and their scales; lane b < 4: record b
+      const int page_tiles = a.v.page_size / TILE_TOKENS;
+      float base = 0.f;
+      bool more = true;
+      int step = s.k0;
+      for (uint32_t n = 0; more; ++n) {
+        if (!__all_sync(0xffffffffu, pt_wait(&bars[TB_LFREE + (n & 3)], ((n >> 2) & 1) ^ 1, abort, a.v.status))) break;
+        const int at = (PT_BN / TILE_TOKENS) * step + lane, keys = s.x.kv_end - PT_BN * step;
+        int rec = -1;
+        float2 sc = make_float2(0.f, 0.f);
+        if (lane < 4 && TILE_TOKENS * lane < keys) {
+          const int idx = at / page_tiles;
+          int page = s.x.b;
+          if (a.v.block_table) page = idx < a.v.max_pages ? a.v.block_table[(size_t)s.x.b * a.v.max_pages + idx] : -1;
+          if (page >= 0 && page < a.v.n_pages) {
+            rec = (page * Hkv + s.kvh) * page_tiles + at % page_tiles;
+            sc = *reinterpret_cast<const float2*>(a.v.pool + (size_t)rec * TILE8_BYTES + TILE8_SCALES);
+          } else if (a.v.status) {
+            atomicOr(a.v.status, IQ_DEVERR_PAGE);
+          }
+        }
+        const bool there = rec >= 0 && sc.y > 0.f;  // (a scale that is no positive number: nothing was written)
+        // log2 in two parts: exact for a power of two
+        const float lv = there ? (float)((int)(__float_as_uint(sc.y) >> 23) - 127) +
+                                     log2f(__uint_as_float((__float_as_uint(sc.y) & 0x7FFFFFu) | 0x3F800000u))
+                               : __uint_as_float(0x7FC00000u);
+        if (step == s.k0) {
+          const uint32_t m = __ballot_sync(0xffffffffu, there);
+          const float first = __shfl_sync(0xffffffffu, lv, m ? __ffs(m) - 1 : 0);
+          base = m ? first : 0.f;
+        }
+        if (lane < 4) {
+          const int i = 4 * (n & 7) + lane;
+          reinterpret_cast<float*>(smem + SM::ks)[i] = sc.x;
+          reinterpret_cast<float*>(smem + SM::lv)[i] = lv;
+          reinterpret_cast<float*>(smem + SM::w)[i] = there ? fast_exp2(base - lv) : 0.f;
+          reinterpret_cast<int*>(smem + SM::rec)[4 * (n & 3) + lane] = rec;
+          if (lane == 0) {
+            reinterpret_cast<float*>(smem + SM::base)[n & 7] = base;
+            reinterpret_cast<int*>(smem + SM::keys)[n & 3] = keys;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[TB_LFULL + (n & 3)]);
+        if (++step == s.k1) {
+          more = s.next(a);
+          step = s.k0;
+        }
+        if (!more) {  // the run's end, for the expansion
+          ++n;
+          if (!__all_sync(0xffffffffu, pt_wait(&bars[TB_LFREE + (n & 3)], ((n >> 2) & 1) ^ 1, abort, a.v.status))) break;
+          if (lane == 0) {
+            reinterpret_cast<int*>(smem + SM::keys)[n & 3] = 0;
+            mbar_arrive(&bars[TB_LFULL + (n & 3)]);
+          }
+        }
+      }
+    } else if (warp == 16) {
     // ==== MMAs: the warp waits together, one lane issues
-    const uint32_t idS = umma_idesc_f16(128, PT_BN), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
+    const uint32_t idS = umma_idesc_f16(128, 64), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
     const uint64_t dq = umma_sdesc_sw128(smem_addr(smem + SM::q)), dk = umma_sdesc_sw128(smem_addr(smem + SM::k)),
                    dv = umma_sdesc_sw128_mn(smem_addr(smem + SM::v), 128);
     uint32_t n = 0, seg = 0, done[2] = {0, 0};
@@ -511,11 +515,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
     auto wait = [&](int bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[bar], parity & 1, abort, a.v.status));
     };
-    auto scores = [&](int t, uint32_t step, bool last) {  // 32 KB (2048 descriptor units) to a tile, to a buffer
+    // scores of tile t's half-step h of step m (the tile's half-step number j): 64 keys, 8192 bytes of a buffer's
+    // blocks (512 descriptor units); tiles and buffers are 32 KB (2048) apart
+    auto scores = [&](int t, uint32_t m, int h, uint32_t j, bool last) {
       if (elect_one()) {
-        umma_f16_k128(tmem + PT_S_COL + 128 * t, dq + 2048 * t, dk + 2048 * (step & 1), idS);
-        umma_commit(&bars[TB_SFULL + t]);
-        if (last) umma_commit(&bars[TB_KFREE + (step & 1)]);
+        umma_f16_k128(tmem + PT_S_COL + 128 * t + 64 * (j & 1), dq + 2048 * t, dk + 2048 * (m & 1) + 512 * h, idS);
+        umma_commit(&bars[TB_SFULL + 2 * t + (j & 1)]);
+        if (last && h) umma_commit(&bars[TB_KFREE + (m & 1)]);
       }
       __syncwarp();
     };
@@ -530,27 +536,29 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       wait(TB_KFULL + (n & 1), n >> 1);
       if (!ok) break;
       tc_fence_after();
-      for (int t = 0; t < tiles; ++t) scores(t, n, t == tiles - 1);
-      for (int i = 0; i < steps && ok; ++i, ++n) {
-        for (int t = 0; t < tiles; ++t) {
-          if (t == 0) wait(TB_VFULL + (n & 1), n >> 1);
-          wait(TB_PFULL + t, done[t]++);
+      for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < tiles; ++t) scores(t, n, h, done[t] + h, t == tiles - 1);
+      // half-step i: O += P V, then the scores of the half-step after the next into the columns that P leaves
+      for (int i = 0; i < 2 * steps && ok; ++i) {
+        const uint32_t m = n + (i >> 1);
+        for (int t = 0; t < tiles; ++t, ++done[t - 1]) {
+          const uint32_t j = done[t];
+          if (t == 0 && !(i & 1)) wait(TB_VFULL + (m & 1), m >> 1);
+          if (t == 0 && !(i & 1) && i + 2 < 2 * steps) wait(TB_KFULL + ((m + 1) & 1), (m + 1) >> 1);
+          wait(TB_PFULL + 2 * t + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            umma_f16_ts_k128(tmem + PT_O_COL + 128 * t, tmem + PT_S_COL + 128 * t, dv + 2048 * (n & 1), idO, i > 0);
-            umma_commit(&bars[TB_ODONE + t]);
-            if (t == tiles - 1) umma_commit(&bars[TB_VFREE + (n & 1)]);
+            umma_f16_ts_k64(tmem + PT_O_COL + 128 * t, tmem + PT_S_COL + 128 * t + 64 * (j & 1),
+                            dv + 2048 * (m & 1) + 512 * (i & 1), idO, i > 0);
+            umma_commit(&bars[TB_ODONE + 2 * t + (j & 1)]);
+            if (t == tiles - 1 && (i & 1)) umma_commit(&bars[TB_VFREE + (m & 1)]);
           }
           __syncwarp();
-          if (i + 1 < steps) {
-            if (t == 0) wait(TB_KFULL + ((n + 1) & 1), (n + 1) >> 1);
-            if (!ok) break;
-            tc_fence_after();
-            scores(t, n + 1, t == tiles - 1);
-          }
+          if (i + 2 < 2 * steps) scores(t, m + 1, i & 1, j + 2, t == tiles - 1);
         }
       }
+      n += steps;
       ++seg;
     } while (ok && s.next(a));
     if (elect_one()) umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released

@@ -51,9 +51,10 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// Eight MMAs over K = 128 from operands in the layouts above, R = 128 rows: the descriptors of the first one, and
-// for the rest the constant steps of their start addresses (in 16-byte units), so that one thread issues them back to
-// back.  A and B along K (two blocks of 64): steps 2, 4, 6, 1024, 1026, ...; D is overwritten.
+// Eight MMAs over K = 128 from operands in the layouts above, R = 128 rows (of which B may take a part): the
+// descriptors of the first one, and for the rest the constant steps of their start addresses (in 16-byte units), so
+// that one thread issues them back to back (72-90 cycles each where it made every descriptor anew, 64 now).  A and B
+// along K (two blocks of 64): steps 2, 4, 6, 1024, 1026, ...; D is overwritten.
 __device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
 #define IQ_UMMA_STEP(off) "add.u64 a, %1, " #off ";\n add.u64 b, %2, " #off ";\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n "
   asm volatile(
@@ -64,15 +65,14 @@ __device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 #undef IQ_UMMA_STEP
 }
-// The same with A (M lanes x 128 binary16 numbers, two to a 32-bit column: eight columns a step) in tensor memory and
-// B along N (2048 bytes a step); D is added to where acc != 0.
-__device__ __forceinline__ void umma_f16_ts_k128(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t acc) {
+// Four MMAs over K = 64 with A (M lanes x 64 binary16 numbers, two to a 32-bit column: eight columns a step) in tensor
+// memory and B along N (2048 bytes a step); D is added to where acc != 0.
+__device__ __forceinline__ void umma_f16_ts_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t acc) {
 #define IQ_UMMA_STEP(i) "add.u32 a, %1, 8 * " #i ";\n add.u64 b, %2, 128 * " #i ";\n tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n "
   asm volatile(
       "{\n .reg .pred p, t;\n .reg .b32 a;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 t, 0, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n " IQ_UMMA_STEP(1) IQ_UMMA_STEP(2) IQ_UMMA_STEP(3)
-      IQ_UMMA_STEP(4) IQ_UMMA_STEP(5) IQ_UMMA_STEP(6) IQ_UMMA_STEP(7) "}\n" ::"r"(d_tmem),
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n " IQ_UMMA_STEP(1) IQ_UMMA_STEP(2) IQ_UMMA_STEP(3) "}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
       : "memory");
 #undef IQ_UMMA_STEP
@@ -134,5 +134,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// The same, tied to the registers that a load fills, so that the compiler moves no use of them before it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                 "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                 "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
+}
 
 }  // namespace iq
