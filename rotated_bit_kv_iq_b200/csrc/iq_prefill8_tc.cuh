@@ -53,11 +53,11 @@ struct PtSmem {
 };
 static_assert(PtSmem::bytes <= 232448, "one CTA's shared memory");
 
-// mbarriers: K and V of step parity expanded / free again; by tile and half-step parity (2 t + b): scores ready, P
-// written, O += P V done (a barrier for each parity: a wait for half-step j knows of j - 2 at the least, so that the
-// phase's parity tells it from the one before); queries; records of step n mod 4 located / taken.
-enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 12, TB_ODONE = 16, TB_Q = 20,
-       TB_DRAIN = 21, TB_LFULL = 22, TB_LFREE = 26, TB_COUNT = 30 };
+// mbarriers: K and V of step parity expanded / free again; by half-step parity: both tiles' scores ready; by tile and
+// half-step parity (2 t + b): P written; the last O += P V done, the one before it; queries; records of step n mod 4
+// located / taken.
+enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 10, TB_ODONE = 14, TB_OLAST = 15,
+       TB_Q = 16, TB_DRAIN = 17, TB_LFULL = 18, TB_LFREE = 22, TB_COUNT = 26 };
 
 struct PtArgs {
   View8 v;
@@ -72,19 +72,22 @@ struct PtArgs {
   float* part_o;    // [2 N][256][128]
 };
 
-// Bounded wait that also ends once another thread has given up.
+// Bounded wait (about 1 s) that also ends once another thread has given up; the global timer is read in one of 4096 tries.
 __device__ __forceinline__ bool pt_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > 1000000000ull) {
-      if (status) atomicOr(status, IQ_DEVERR_TIMEOUT);
-      *abort = 1;
-      return false;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0 && *abort) return false;
+    if ((i & 4095u) == 0) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 1000000000ull) {
+        if (status) atomicOr(status, IQ_DEVERR_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
     }
   }
-  return true;
 }
 
 // Entry e = (sequence, block of tokens): where its rows and keys are.
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         const int halves = 2 * (s.k1 - s.k0);
         for (int i = 0; i < halves; ++i, ++done) {
           const int buf = done & 1;
-          ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + 2 * t + buf], (done >> 1) & 1, abort, a.v.status));
+          ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + buf], (done >> 1) & 1, abort, a.v.status));
           if (!ok) break;
           tc_fence_after();
           const int slot = 2 * ((n + (i >> 1)) & 7) + (i & 1);
@@ -329,7 +332,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
             const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
             if (up) ref = mo;
             if (i > 0) {
-              ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + 2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort, a.v.status));
+              // O += P V of the half-step before is done: the scores of the next one, or at the end a barrier of its
+              // own, are signalled after it
+              const bool next = i + 1 < halves;
+              ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
+                                                : pt_wait(&bars[TB_ODONE], seg & 1, abort, a.v.status));
               if (!ok) break;
               tc_fence_after();
               l *= al;
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[TB_PFULL + 2 * t + buf]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_ODONE + 2 * t + ((done - 1) & 1)], ((done - 1) >> 1) & 1, abort, a.v.status));
+        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_OLAST], seg & 1, abort, a.v.status));
         if (!ok) break;
         tc_fence_after();
         const bool whole = s.k0 == 0 && s.k1 == s.x.steps;
@@ -382,8 +389,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         __syncwarp();
         tc_fence_before();
       } else {  // no row of this tile: not ahead of the tile that has rows
-        ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_Q], seg & 1, abort, a.v.status));
+        ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_OLAST], seg & 1, abort, a.v.status));
         if (!ok) break;
+        done += 2 * (s.k1 - s.k0);
       }
       n += s.k1 - s.k0;
       ++seg;
@@ -506,64 +514,82 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         }
       }
     } else if (warp == 16) {
-    // ==== MMAs: the warp waits together, one lane issues
-    const uint32_t idS = umma_idesc_f16(128, 64), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
-    const uint64_t dq = umma_sdesc_sw128(smem_addr(smem + SM::q)), dk = umma_sdesc_sw128(smem_addr(smem + SM::k)),
-                   dv = umma_sdesc_sw128_mn(smem_addr(smem + SM::v), 128);
-    uint32_t n = 0, seg = 0, done[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](int bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[bar], parity & 1, abort, a.v.status));
-    };
-    // scores of tile t's half-step h of step m (the tile's half-step number j): 64 keys, 8192 bytes of a buffer's
-    // blocks (512 descriptor units); tiles and buffers are 32 KB (2048) apart
-    auto scores = [&](int t, uint32_t m, int h, uint32_t j, bool last) {
-      if (elect_one()) {
-        umma_f16_k128(tmem + PT_S_COL + 128 * t + 64 * (j & 1), dq + 2048 * t, dk + 2048 * (m & 1) + 512 * h, idS);
-        umma_commit(&bars[TB_SFULL + 2 * t + (j & 1)]);
-        if (last && h) umma_commit(&bars[TB_KFREE + (m & 1)]);
-      }
-      __syncwarp();
-    };
-    do {
-      const int tiles = s.x.n_live * G > PT_TILE ? 2 : 1, steps = s.k1 - s.k0;
-      if (lane == 0) {  // where the block is cut, for the merge
-        int2* const cut = a.cut + (size_t)s.e * Hkv + s.kvh;
-        if (s.k0 == 0) cut->x = 2 * c + (s.pos == 0 ? 0 : 1);
-        if (s.k1 == s.x.steps) cut->y = c;
-      }
-      wait(TB_Q, seg);
-      wait(TB_KFULL + (n & 1), n >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      for (int h = 0; h < 2; ++h)
-        for (int t = 0; t < tiles; ++t) scores(t, n, h, done[t] + h, t == tiles - 1);
-      // half-step i: O += P V, then the scores of the half-step after the next into the columns that P leaves
-      for (int i = 0; i < 2 * steps && ok; ++i) {
-        const uint32_t m = n + (i >> 1);
-        for (int t = 0; t < tiles; ++t, ++done[t - 1]) {
-          const uint32_t j = done[t];
-          if (t == 0 && !(i & 1)) wait(TB_VFULL + (m & 1), m >> 1);
-          if (t == 0 && !(i & 1) && i + 2 < 2 * steps) wait(TB_KFULL + ((m + 1) & 1), (m + 1) >> 1);
-          wait(TB_PFULL + 2 * t + (j & 1), j >> 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            umma_f16_ts_k64(tmem + PT_O_COL + 128 * t, tmem + PT_S_COL + 128 * t + 64 * (j & 1),
-                            dv + 2048 * (m & 1) + 512 * (i & 1), idO, i > 0);
-            umma_commit(&bars[TB_ODONE + 2 * t + (j & 1)]);
-            if (t == tiles - 1 && (i & 1)) umma_commit(&bars[TB_VFREE + (m & 1)]);
-          }
-          __syncwarp();
-          if (i + 2 < 2 * steps) scores(t, m + 1, i & 1, j + 2, t == tiles - 1);
+      // ==== MMAs.  The tensor core takes its operands' descriptors from uniform registers: the warp runs as one, on
+      // counts that are broadcast and in loops without an early end (where a wait has given up the others do too, soon,
+      // and what is computed then is nobody's), so that the compiler keeps them there.  With descriptors from one
+      // lane's registers an MMA took about 94 cycles to issue, not 52.
+      const uint32_t idS = umma_idesc_f16(128, 64), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
+      const uint64_t dq = umma_sdesc_sw128(sm + SM::q), dk = umma_sdesc_sw128(sm + SM::k), dv = umma_sdesc_sw128_mn(sm + SM::v, 128);
+      uint32_t n = 0, seg = 0, written[2] = {0, 0};  // steps, segments; half-steps of P by tile
+      auto wait = [&](int bar, uint32_t parity) {
+        pt_wait(&bars[bar], parity & 1, abort, a.v.status);
+        __syncwarp();
+      };
+      // scores of tile t's half-step h of step m: 64 keys, 8192 bytes of a buffer's blocks (512 descriptor units); tiles
+      // and buffers are 32 KB (2048) apart
+      auto scores = [&](int t, uint32_t m, int h) {
+        umma_f16_k128(tm + PT_S_COL + 128 * t + 64 * h, dq + 2048 * t, dk + 2048 * (m & 1) + 512 * h, idS);
+      };
+      bool more = true;
+      do {
+        const int tiles = __shfl_sync(0xffffffffu, s.x.n_live * G > PT_TILE ? 2 : 1, 0);
+        const int steps = __shfl_sync(0xffffffffu, s.k1 - s.k0, 0);
+        if (lane == 0) {  // where the block is cut, for the merge
+          int2* const cut = a.cut + (size_t)s.e * Hkv + s.kvh;
+          if (s.k0 == 0) cut->x = 2 * c + (s.pos == 0 ? 0 : 1);
+          if (s.k1 == s.x.steps) cut->y = c;
         }
-      }
-      n += steps;
-      ++seg;
-    } while (ok && s.next(a));
-    if (elect_one()) umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released
-    __syncwarp();
-    mbar_wait(&bars[TB_DRAIN], 0, nullptr);
+        wait(TB_Q, seg);
+        wait(TB_KFULL + (n & 1), n >> 1);
+        tc_fence_after();
+        if (elect_one()) {
+          scores(0, n, 0);
+          if (tiles == 2) scores(1, n, 0);
+          umma_commit(&bars[TB_SFULL]);
+          scores(0, n, 1);
+          if (tiles == 2) scores(1, n, 1);
+          umma_commit(&bars[TB_SFULL + 1]);
+          umma_commit(&bars[TB_KFREE + (n & 1)]);
+        }
+        __syncwarp();
+        // a step's half-steps b: O += P V, then the scores of the next step's half b into the columns that P leaves
+        for (int i = 0; i < steps; ++i, ++n) {
+          const bool last = i + 1 == steps;
+          wait(TB_VFULL + (n & 1), n >> 1);
+          if (!last) wait(TB_KFULL + ((n + 1) & 1), (n + 1) >> 1);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t < tiles) {
+                wait(TB_PFULL + 2 * t + b, written[t] >> 1);
+                ++written[t];
+                tc_fence_after();
+                if (elect_one()) {
+                  umma_f16_ts_k64(tm + PT_O_COL + 128 * t, tm + PT_S_COL + 128 * t + 64 * b, dv + 2048 * (n & 1) + 512 * b, idO, i + b > 0);
+                  if (!last) scores(t, n + 1, b);
+                }
+                __syncwarp();
+              }
+            }
+            if (elect_one()) {
+              if (!last) umma_commit(&bars[TB_SFULL + b]);
+              else umma_commit(&bars[b ? TB_OLAST : TB_ODONE]);
+              if (b) {
+                umma_commit(&bars[TB_VFREE + (n & 1)]);
+                if (!last) umma_commit(&bars[TB_KFREE + ((n + 1) & 1)]);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        ++seg;
+        more = __shfl_sync(0xffffffffu, (int)s.next(a), 0);
+      } while (more);
+      if (elect_one()) umma_commit(&bars[TB_DRAIN]);  // every MMA issued is complete before tensor memory is released
+      __syncwarp();
+      mbar_wait(&bars[TB_DRAIN], 0, nullptr);
     }
   }
   tc_fence_before();
