@@ -598,38 +598,62 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
   if (warp == 16) tmem_free(tmem, 512);
 }
 
-// Merge of the blocks that were cut: a warp per row, its partials in order.
-static __global__ void __launch_bounds__(256) prefill8_merge_kernel(PtArgs a) {
+// Merge of the blocks that were cut: a warp takes four rows at a time, their partials in order.  Bound by the partials'
+// reading; four rows' loads in flight a warp (one row's: 24 us for the 2048-token chunk's 147 cut blocks).
+constexpr int PTM_WARPS = 8, PTM_ROWS = 4, PTM_TIMES = 2;  // rows of a CTA: their product
+static __global__ void __launch_bounds__(32 * PTM_WARPS) prefill8_merge_kernel(PtArgs a) {
   pdl_wait();
   const int Hkv = a.v.n_kv_heads, G = a.g_real;
+  const int2 cut = a.cut[blockIdx.x];
   const int e = blockIdx.x / Hkv, kvh = blockIdx.x % Hkv;
   const PtEntry x = pt_entry(a, e);
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= x.n_live * G) return;
-  const int2 cut = a.cut[blockIdx.x];
+  const int lane = threadIdx.x & 31, rows = x.n_live * G;
+  if (rows == 0) return;
   // (clamped: after a timeout they may not have been written)
   const int first = max(0, min(2 * a.ctas - 1, cut.x)), c0 = first >> 1, c1 = max(c0, min(a.ctas - 1, cut.y));
   if (c0 == c1) return;
-  auto row_of = [&](int k) { return (size_t)(k == c0 ? first : 2 * k) * PT_ROWS + r; };
-  float M = -CUDART_INF_F, MO = -CUDART_INF_F;
-  for (int k = c0; k <= c1; ++k) {
-    const float4 ml = a.part_ml[row_of(k)];
-    M = fmaxf(M, ml.x);
-    MO = fmaxf(MO, ml.y);
+#pragma unroll 1
+  for (int i = 0; i < PTM_TIMES; ++i) {
+    const int r0 = ((blockIdx.y * PTM_TIMES + i) * PTM_WARPS + (threadIdx.x >> 5)) * PTM_ROWS;
+    if (r0 >= rows) return;
+    float M[PTM_ROWS], MO[PTM_ROWS], L[PTM_ROWS];
+    float4 o[PTM_ROWS];
+#pragma unroll
+    for (int j = 0; j < PTM_ROWS; ++j) {
+      M[j] = MO[j] = -CUDART_INF_F;
+      L[j] = 0.f;
+      o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int k = c0; k <= c1; ++k) {
+      const size_t slot = (size_t)(k == c0 ? first : 2 * k) * PT_ROWS + r0;
+      float4 ml[PTM_ROWS], y[PTM_ROWS];
+#pragma unroll
+      for (int j = 0; j < PTM_ROWS; ++j) {  // (rows behind the block's last, up to a tile's end, hold neutral partials)
+        const bool live = r0 + j < rows;
+        ml[j] = live ? a.part_ml[slot + j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        y[j] = live ? reinterpret_cast<const float4*>(a.part_o + (slot + j) * D)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < PTM_ROWS; ++j) {
+        if (ml[j].z == 0.f) continue;
+        const float m = fmaxf(M[j], ml[j].x), mo = fmaxf(MO[j], ml[j].y);
+        const float fl = M[j] == -CUDART_INF_F ? 0.f : fast_exp2(M[j] - m), fo = MO[j] == -CUDART_INF_F ? 0.f : fast_exp2(MO[j] - mo);
+        const float wl = fast_exp2(ml[j].x - m), wo = fast_exp2(ml[j].y - mo);
+        L[j] = L[j] * fl + ml[j].z * wl;
+        o[j] = make_float4(o[j].x * fo + y[j].x * wo, o[j].y * fo + y[j].y * wo, o[j].z * fo + y[j].z * wo, o[j].w * fo + y[j].w * wo);
+        M[j] = m;
+        MO[j] = mo;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PTM_ROWS; ++j) {
+      const int r = r0 + j;
+      if (r >= rows) break;
+      const float f = L[j] > 0.f ? fast_exp2(MO[j] - M[j]) / L[j] : (L[j] == L[j] ? 0.f : L[j]);
+      const size_t row = ((size_t)x.b * a.n_tok + x.tok0 + r / G) * a.n_q_heads + (size_t)kvh * G + r % G;
+      store4(a.out, a.dtype, row * D + 4 * lane, make_float4(o[j].x * f, o[j].y * f, o[j].z * f, o[j].w * f));
+    }
   }
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = c0; k <= c1; ++k) {
-    const float4 ml = a.part_ml[row_of(k)];
-    if (ml.z == 0.f) continue;
-    const float4 y = reinterpret_cast<const float4*>(a.part_o + row_of(k) * D)[lane];
-    L += ml.z * fast_exp2(ml.x - M);
-    const float f = fast_exp2(ml.y - MO);
-    o.x = fmaf(y.x, f, o.x); o.y = fmaf(y.y, f, o.y); o.z = fmaf(y.z, f, o.z); o.w = fmaf(y.w, f, o.w);
-  }
-  const float f = L > 0.f ? fast_exp2(MO - M) / L : (L == L ? 0.f : L);
-  const size_t row = ((size_t)x.b * a.n_tok + x.tok0 + r / G) * a.n_q_heads + (size_t)kvh * G + r % G;
-  store4(a.out, a.dtype, row * D + 4 * lane, make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
 }
 
 struct PtPlan {
@@ -676,9 +700,9 @@ inline int launch_prefill8_tc(const View8& v, const void* q, int dtype, int batc
   if (e != cudaSuccess) return (int)e;
   e = launch_pdl(fn, dim3(p.ctas), dim3(PT_THREADS), PtSmem::bytes, (cudaStream_t)stream, a);
   if (e != cudaSuccess || p.ctas == 1) return (int)e;
-  const int rows = std::min(n_tok, p.tq) * a.g_real;
-  return (int)launch_pdl(prefill8_merge_kernel, dim3((unsigned)(batch * p.n_blk * v.n_kv_heads), (rows + 7) / 8), dim3(256), 0,
-                         (cudaStream_t)stream, a);
+  const int rows = std::min(n_tok, p.tq) * a.g_real, per = PTM_WARPS * PTM_ROWS * PTM_TIMES;
+  return (int)launch_pdl(prefill8_merge_kernel, dim3((unsigned)(batch * p.n_blk * v.n_kv_heads), (rows + per - 1) / per),
+                         dim3(32 * PTM_WARPS), 0, (cudaStream_t)stream, a);
 }
 
 }  // namespace iq
