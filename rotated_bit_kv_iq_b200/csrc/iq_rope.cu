@@ -98,50 +98,61 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& a, int n, float2* cs
 }
 
 // LAYOUT interleaved: an item is eight neighbouring coordinates (four pairs).  LAYOUT half (rotary_dim / 2 a
-// multiple of 8): an item is eight coordinates of the first half and their partners; behind the rotary part
-// an item is eight coordinates to copy.
+// multiple of 8): an item is eight coordinates of the first half and their partners; behind the rotary part an item
+// is eight coordinates to copy.  A thread's items are loaded four at a time, the first four before the angles.
 template <int DT, int LAYOUT>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeArgs a) {
+  constexpr int U = 4;
   __shared__ float2 cs[D / 2];
   pdl_wait();
   const int n = blockIdx.x, half = a.rd / 2;
   const int turn = LAYOUT == IQ_ROPE_HALF ? half / 8 : D / 8;               // items of a head that turn
   const int items = LAYOUT == IQ_ROPE_HALF ? turn + (D - a.rd) / 8 : turn;  // and all of them
-  const int total = (a.heads[0] + a.heads[1]) * items;
-  rope_angles(a, n, cs);
-  __syncthreads();
-  for (int i = threadIdx.x; i < total; i += ROPE_THREADS) {
-    int h = i / items;
-    const int it = i % items;
-    const int side = h >= a.heads[0];
-    if (side) h -= a.heads[0];
-    const long long src = n * a.xs[side] + h * D, dst = n * a.ys[side] + h * D;
-    if (LAYOUT == IQ_ROPE_HALF) {
-      if (it >= turn) {
-        const int c = a.rd + 8 * (it - turn);
-        rope_store<DT>(a.y[side], dst + c, rope_load<DT>(a.x[side], src + c));
-        continue;
-      }
-      const int c = 8 * it;
-      const RopeVec<DT> u = rope_load<DT>(a.x[side], src + c), w = rope_load<DT>(a.x[side], src + half + c);
-      float x[8], y[8];
-      rope_widen<DT>(u, x);
-      rope_widen<DT>(w, y);
+  const int nq = a.heads[0] * items, total = nq + a.heads[1] * items;
+  const uint8_t* const xq = (const uint8_t*)a.x[0] + n * a.xs[0] * (DT == IQ_F32 ? 4 : 2);
+  const uint8_t* const xk = (const uint8_t*)a.x[1] + n * a.xs[1] * (DT == IQ_F32 ? 4 : 2);
+  uint8_t* const yq = (uint8_t*)a.y[0] + n * a.ys[0] * (DT == IQ_F32 ? 4 : 2);
+  uint8_t* const yk = (uint8_t*)a.y[1] + n * a.ys[1] * (DT == IQ_F32 ? 4 : 2);
+  for (int i0 = threadIdx.x; i0 < total || i0 == threadIdx.x; i0 += U * ROPE_THREADS) {
+    RopeVec<DT> u[U], w[LAYOUT == IQ_ROPE_HALF ? U : 1];
+    int at[U];  // the item's first coordinate in its head, its head's place added
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 t = cs[c + k];
-        const float p = x[k] * t.x - y[k] * t.y, q = x[k] * t.y + y[k] * t.x;
-        x[k] = p;
-        y[k] = q;
-      }
-      rope_store<DT>(a.y[side], dst + c, rope_narrow<DT>(x));
-      rope_store<DT>(a.y[side], dst + half + c, rope_narrow<DT>(y));
-    } else {
-      const int c = 8 * it;
-      RopeVec<DT> u = rope_load<DT>(a.x[side], src + c);
-      if (c < a.rd) {
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * ROPE_THREADS, k = i >= nq, h = (k ? i - nq : i) / items, it = (k ? i - nq : i) % items;
+      at[j] = h * D + (LAYOUT == IQ_ROPE_HALF && it >= turn ? a.rd + 8 * (it - turn) : 8 * it);
+      if (i >= total) continue;
+      u[j] = rope_load<DT>(k ? xk : xq, at[j]);
+      if (LAYOUT == IQ_ROPE_HALF && it < turn) w[LAYOUT == IQ_ROPE_HALF ? j : 0] = rope_load<DT>(k ? xk : xq, at[j] + half);
+    }
+    if (i0 == threadIdx.x) {
+      rope_angles(a, n, cs);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = i0 + j * ROPE_THREADS;
+      if (i >= total) break;
+      uint8_t* const y = i >= nq ? yk : yq;
+      const int c = at[j] % D;
+      if (LAYOUT == IQ_ROPE_HALF) {
+        if (c < half) {
+          RopeVec<DT>& v = w[LAYOUT == IQ_ROPE_HALF ? j : 0];
+          float x0[8], x1[8];
+          rope_widen<DT>(u[j], x0);
+          rope_widen<DT>(v, x1);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 t = cs[c + k];
+            const float p = x0[k] * t.x - x1[k] * t.y, q = x0[k] * t.y + x1[k] * t.x;
+            x0[k] = p;
+            x1[k] = q;
+          }
+          u[j] = rope_narrow<DT>(x0);
+          rope_store<DT>(y, at[j] + half, rope_narrow<DT>(x1));
+        }
+      } else if (c < a.rd) {
         float x[8];
-        rope_widen<DT>(u, x);
+        rope_widen<DT>(u[j], x);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (c + 2 * k >= a.rd) continue;
@@ -150,9 +161,9 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(RopeArgs a) {
           x[2 * k] = p;
           x[2 * k + 1] = q;
         }
-        u = rope_narrow<DT>(x);
+        u[j] = rope_narrow<DT>(x);
       }
-      rope_store<DT>(a.y[side], dst + c, u);
+      rope_store<DT>(y, at[j], u[j]);
     }
   }
 }
