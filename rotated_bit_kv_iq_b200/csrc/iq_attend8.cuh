@@ -75,8 +75,9 @@ __device__ __forceinline__ float load_q8(const void* q, int dtype, size_t row, b
 }
 
 // The tile at `tile` (shared memory) into r: row g sees the first `lim` tokens.  The codes of V rows that
-// no row sees must be finite (zeroed by the caller).
-template <int CODE>
+// no row sees must be finite (zeroed by the caller).  FEW (at most four heads): rows 4-7 repeat rows 0-3 and carry the
+// lo terms of P, so that one product does for both (48 instead of 64 MMAs a tile).
+template <int CODE, bool FEW>
 __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32_t qa[8][4], float qs, Row8& r) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const float ks = reinterpret_cast<const float*>(tile + TILE8_SCALES)[0] * qs;
@@ -132,6 +133,7 @@ __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32
     ph[n] = half2_bits(x0, x1);
     const float2 h = half2_floats(ph[n]);
     pl[n] = half2_bits(x0 - h.x, x1 - h.y);
+    if (FEW && g >= 4) ph[n] = pl[n];
   }
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
@@ -150,7 +152,7 @@ __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32
         codes4_to_half2x2<CODE>(prmt(x0[w], x1[w], sel), a[0], a[1]);
         codes4_to_half2x2<CODE>(prmt(x2[w], x3[w], sel), a[2], a[3]);
         hmma8(r.o[2 * w + h], a, ph[2 * kk], ph[2 * kk + 1]);
-        hmma8(r.o[2 * w + h], a, pl[2 * kk], pl[2 * kk + 1]);
+        if (!FEW) hmma8(r.o[2 * w + h], a, pl[2 * kk], pl[2 * kk + 1]);
       }
     }
   }
@@ -163,7 +165,8 @@ __device__ __forceinline__ void clear_v_rows8(uint8_t* tile, int n) {
   __syncwarp();
 }
 
-// The warp's state into shared memory: (m, mo, l) per row, and rows of 128 sums.
+// The warp's state into shared memory: (m, mo, l) per row, and rows of 128 sums (FEW: of four rows).
+template <bool FEW>
 __device__ __forceinline__ void row8_store(Row8& r, float (*ml)[4], float* so) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float l = r.l + __shfl_xor_sync(0xffffffffu, r.l, 1);
@@ -172,6 +175,13 @@ __device__ __forceinline__ void row8_store(Row8& r, float (*ml)[4], float* so) {
     ml[g][0] = r.m;
     ml[g][1] = r.mo;
     ml[g][2] = l;
+  }
+  if (FEW) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.o[i][e] += __shfl_xor_sync(0xffffffffu, r.o[i][e], 2);
+    if (t >= 2) return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -65,10 +65,10 @@ __global__ void __launch_bounds__(P8_WARPS * 32) prefill8_kernel(Prefill8Args a)
     __syncwarp();
     const int n_valid = min(TILE_TOKENS, ctx - tile * TILE_TOKENS);
     if (n_valid < TILE_TOKENS) clear_v_rows8(t, n_valid);
-    tile8<CODE>(t, min(TILE_TOKENS, seen - tile * TILE_TOKENS), qa, qs, r);
+    tile8<CODE, false>(t, min(TILE_TOKENS, seen - tile * TILE_TOKENS), qa, qs, r);
   }
   float* const so = reinterpret_cast<float*>(smem + P8_WARPS * TILE8_BYTES);
-  row8_store(r, sml[warp], so + warp * A8_ROWS * D);
+  row8_store<false>(r, sml[warp], so + warp * A8_ROWS * D);
   __syncthreads();
   for (int x = warp; x < TQ * G; x += P8_WARPS) {
     if (x / G >= n_live) continue;

@@ -251,6 +251,33 @@ def test_decode_over_many_splits_and_many_sequences(batch, hkv, lens):
         _check_rows(o[b], q[b].double().numpy(), np.stack([x[0] for x in kv]), np.stack([x[1] for x in kv]), 0.05, F32)
 
 
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+def test_decode_with_many_tiles_a_cta(code):
+    """More tiles to a CTA than it has in flight at once, in segments of several groups, some of a tile or two."""
+    lens = [6000, 33, 5000, 1, 7001, 0, 6400, 64, 4097]
+    hkv, ps, per = 4, 64, 112
+    c = B.PagedCache8(1, hkv, ps, len(lens) * per, code=code, block_table=torch.randperm(
+        len(lens) * per, generator=torch.Generator().manual_seed(3)).view(-1, per).to(torch.int32).to(DEV))
+    c.pool.fill_(0x7F)
+    k, v = (_tokens(s, (len(lens), max(lens), hkv, 128)).to(DEV) for s in (4, 5))
+    B.iq_append8(c, 0, k, v, _i32([0] * len(lens)), _i32(lens))
+    for G, dtype in ((4, F16), (8, F32)):
+        q = torch.randn((len(lens), G * hkv, 128), generator=torch.Generator().manual_seed(2)).to(dtype)
+        out = torch.full_like(q, float("nan")).to(DEV)
+        ws = torch.zeros(B.iq_decode8_workspace_size(len(lens), G * hkv, hkv, ps * per), dtype=torch.uint8, device=DEV)
+        for _ in range(3):
+            B.iq_decode8_attention(c, 0, q.to(DEV), _i32(lens), ps * per, out, ws)
+        o = out.double().cpu().numpy()
+        assert c.status.item() == 0
+        for b, n in enumerate(lens):
+            kv = []
+            for side in (0, 1):
+                x = torch.empty((hkv, n, 128), dtype=F32, device=DEV)
+                B.iq_export8(c, 0, side, b, 0, n, x)
+                kv.append(x.double().cpu().numpy())
+            _check_rows(o[b], q[b].double().numpy(), *kv, 128 ** -0.5, dtype)
+
+
 @pytest.mark.parametrize("lens", [[0, 0], [1, 0], [40, 700], [3, 260]])
 def test_lengths_far_below_the_bound(lens):
     """max_ctx sizes the grid; the lengths decide what there is to share out."""
