@@ -86,24 +86,30 @@ __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32
   const float vman = __uint_as_float((vsb & 0x7FFFFFu) | 0x3F800000u);
   float s[8];
   float mx = -CUDART_INF_F;
+  float d[4][4];
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const uint4 w0 = *reinterpret_cast<const uint4*>(tile + chunk8(8 * n + g, 2 * t));
-    const uint4 w1 = *reinterpret_cast<const uint4*>(tile + chunk8(8 * n + g, 2 * t + 1));
-    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < 4; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t b0, b1;
-      codes4_to_half2x2<CODE>(w[i], b0, b1);
-      hmma8(d, qa[i], b0, b1);
-    }
+  for (int c = 0; c < 2; ++c) {  // the four token groups side by side: four independent chains of MMAs
+    uint4 k[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) k[n] = *reinterpret_cast<const uint4*>(tile + chunk8(8 * n + g, 2 * t + c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t b0, b1;
+        codes4_to_half2x2<CODE>(i == 0 ? k[n].x : i == 1 ? k[n].y : i == 2 ? k[n].z : k[n].w, b0, b1);
+        hmma8(d[n], qa[4 * c + i], b0, b1);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[2 * n + e] = 8 * n + 2 * t + e < lim ? (d[e] + d[2 + e]) * ks : -CUDART_INF_F;
+      s[2 * n + e] = 8 * n + 2 * t + e < lim ? (d[n][e] + d[n][2 + e]) * ks : -CUDART_INF_F;
       mx = fmaxf(mx, s[2 * n + e]);
     }
-  }
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   const float m = fmaxf(r.m, mx), mo = fmaxf(r.mo, mx + vexp);
