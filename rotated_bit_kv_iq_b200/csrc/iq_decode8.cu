@@ -1,6 +1,8 @@
-// Decode attention over the 8-bit cache: one query token per sequence.
+// Attention over the 8-bit cache of few query rows: one token of each sequence (decode), or a chunk of float32 tokens in
+// blocks of up to eight rows.
 //
-// The work is the list of 32-token tiles of all (sequence, kv head) groups; CTA c of N takes tiles
+// The work is the list of 32-token tiles of all (entry, kv head) groups, an entry being a sequence or
+// a block of its query tokens; CTA c of N takes tiles
 // [c T / N, (c + 1) T / N), whatever the mix of lengths.  Its warps take the tiles of each group's segment in turn, each
 // through a ring of its own of two bulk-copied tile records: twelve warps, three a scheduler, at 168 registers.  On the
 // 16-sequence layer: PLACEHOLDER_SERVE us, 105 with eight warps (197 registers); 121 with sixteen (128 registers, which
@@ -23,18 +25,41 @@ struct Decode8Args {
   View8 v;
   const void* q;
   int dtype, batch, n_q_heads, g_real, max_ctx;
-  const int32_t* ctx_len;
+  const int32_t* ctx_len;  // decode; or, with ctx_len NULL, blocks of tq of a chunk's n_tok tokens, n_blk a sequence:
+  int n_tok, tq, n_blk;
+  const int32_t* start;
+  const int32_t* n_valid;
   float scale;
   void* out;
-  int32_t* counters;  // [batch * Hkv], zero between calls
+  int32_t* counters;  // [batch * n_blk * Hkv], zero between calls
   float4* part_ml;    // [2 N][8]: m, mo, l
   float* part_o;      // [2 N][8][128]
 };
 
-__device__ __forceinline__ int clamp_ctx8(const Decode8Args& a, int b) {
-  const int c = a.ctx_len[b];
-  return c < 0 ? 0 : (c > a.max_ctx ? a.max_ctx : c);
+// Entry e: a sequence (decode), or a block of a sequence's query tokens.
+struct D8Entry {
+  int b, tok0, n_live, pos0, ctx;  // its tokens, the first one's position, the keys that the last one sees
+};
+__device__ __forceinline__ D8Entry d8_entry(const Decode8Args& a, int e) {
+  D8Entry x;
+  if (a.ctx_len) {
+    const int c = a.ctx_len[e];
+    x.b = e;
+    x.tok0 = 0;
+    x.n_live = 1;
+    x.ctx = c < 0 ? 0 : (c > a.max_ctx ? a.max_ctx : c);
+    x.pos0 = x.ctx - 1;
+  } else {
+    x.b = e / a.n_blk;
+    x.tok0 = e % a.n_blk * a.tq;
+    const int cnt = max(0, min(a.n_tok, a.n_valid ? a.n_valid[x.b] : a.n_tok));
+    x.n_live = max(0, min(a.tq, cnt - x.tok0));
+    x.pos0 = max(0, min(a.max_ctx - cnt, a.start[x.b])) + x.tok0;
+    x.ctx = x.n_live ? x.pos0 + x.n_live : 0;
+  }
+  return x;
 }
+__device__ __forceinline__ int d8_tiles(const Decode8Args& a, int e) { return (d8_entry(a, e).ctx + TILE_TOKENS - 1) / TILE_TOKENS; }
 
 // Final value of one row of the group: lane holds sums of coordinates 4 lane ..
 __device__ __forceinline__ void finish_row8(const Decode8Args& a, size_t row, float M, float MO, float L, float4 o) {
@@ -48,7 +73,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __shared__ __align__(8) uint64_t bars[D8_WARPS][D8_NB];
   __shared__ float sml[D8_WARPS][A8_ROWS][4];
   __shared__ long long s_scan[D8_WARPS];
-  __shared__ int s_start[2];  // the CTA's first sequence, and the tiles before it within all kv heads
+  __shared__ int s_most[D8_WARPS];
+  __shared__ int s_start[2];  // the CTA's first entry, and the tiles before it within all kv heads
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
@@ -61,9 +87,16 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   pdl_wait();
 
   // ---- plan: total tiles, this CTA's range, the sequence that it starts in
-  const int per = (a.batch + D8_THREADS - 1) / D8_THREADS, b0 = tid * per;
+  const int E = a.batch * a.n_blk, per = (E + D8_THREADS - 1) / D8_THREADS, e0 = min(E, tid * per), e1 = min(E, e0 + per);
   long long mine = 0;
-  for (int b = b0; b < min(a.batch, b0 + per); ++b) mine += (clamp_ctx8(a, b) + TILE_TOKENS - 1) / TILE_TOKENS;
+  int most = 0;  // tiles of an entry
+  for (int e = e0; e < e1; ++e) {
+    const int n = d8_tiles(a, e);
+    mine += n;
+    most = max(most, n);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) s_most[warp] = most;
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -76,49 +109,84 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   for (int w = 0; w < D8_WARPS; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
+    most = max(most, s_most[w]);
   }
   before *= Hkv;
   total *= Hkv;
   // the CTAs that share the tiles: none without one, and no more than give every warp one
   const int N = (int)min((long long)gridDim.x, max(1ll, (total + D8_WARPS - 1) / D8_WARPS));
   const long long lo = c < N ? c * total / N : total, hi = c < N ? (c + 1) * total / N : total;
-  long long acc = before;  // tiles of all groups before sequence b
-  for (int b = b0; b < min(a.batch, b0 + per); ++b) {
-    const long long nt = (long long)Hkv * ((clamp_ctx8(a, b) + TILE_TOKENS - 1) / TILE_TOKENS);
-    if (lo < hi && acc <= lo && lo < acc + nt) {
-      s_start[0] = b;
+  long long acc = before;  // tiles of all groups before entry e
+  for (int e = e0; e < e1 && acc <= lo; ++e) {
+    const long long n = (long long)Hkv * d8_tiles(a, e);
+    if (lo < hi && lo < acc + n) {
+      s_start[0] = e;
       s_start[1] = (int)(lo - acc);
     }
-    acc += nt;
+    acc += n;
   }
-  if (c == 0 && a.v.status)
-    for (int b = tid; b < a.batch; b += D8_THREADS)
-      if (clamp_ctx8(a, b) != a.ctx_len[b]) atomicOr(a.v.status, IQ_DEVERR_CTX);
+  if (c == 0 && a.v.status)  // lengths, counts and starts outside their ranges
+    for (int b = tid; b < a.batch; b += D8_THREADS) {
+      bool bad;
+      if (a.ctx_len) {
+        bad = a.ctx_len[b] < 0 || a.ctx_len[b] > a.max_ctx;
+      } else {
+        const int cnt = a.n_valid ? a.n_valid[b] : a.n_tok, st = a.start[b];
+        bad = cnt < 0 || cnt > a.n_tok || st < 0 || st > a.max_ctx - max(0, min(a.n_tok, cnt));
+      }
+      if (bad) atomicOr(a.v.status, IQ_DEVERR_CTX);
+    }
   // sequences with nothing to see: zero rows
-  for (int b = c; b < a.batch; b += gridDim.x)
-    if (clamp_ctx8(a, b) == 0)
-      for (int i = tid; i < a.n_q_heads * (D / 4); i += D8_THREADS)
-        store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+  if (a.ctx_len)
+    for (int b = c; b < a.batch; b += gridDim.x)
+      if (d8_entry(a, b).ctx == 0)
+        for (int i = tid; i < a.n_q_heads * (D / 4); i += D8_THREADS)
+          store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   __syncthreads();
-  if (lo >= hi) return;
-
-  int b = s_start[0];
-  int ctx = clamp_ctx8(a, b), nt = (ctx + TILE_TOKENS - 1) / TILE_TOKENS;
-  int kvh = s_start[1] / nt, tile0 = s_start[1] % nt;
-  long long pos = lo;
+  // Short groups, of two rounds of the warps at the most, are not cut: CTA c takes groups c, c + grid, ... whole, and there
+  // is nothing to merge (a 512-token layer of two kv heads: PLACEHOLDER_SHORT).
+  const bool uncut = most <= 2 * D8_WARPS;
+  if (!uncut && lo >= hi) return;
+  int e = 0, kvh = 0, nt = 0, tile0 = 0;
+  D8Entry x = {};
+  long long pos = lo, gi = c;
+  auto take = [&]() {  // uncut: the next group that has tiles, from gi on; whether there is one
+    for (; gi < (long long)E * Hkv; gi += gridDim.x) {
+      e = (int)(gi / Hkv);
+      kvh = (int)(gi % Hkv);
+      x = d8_entry(a, e);
+      nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
+      if (nt) return true;
+    }
+    return false;
+  };
+  bool more;
+  if (uncut) {
+    more = take();
+  } else {
+    e = s_start[0];
+    x = d8_entry(a, e);
+    nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
+    kvh = s_start[1] / nt;
+    tile0 = s_start[1] % nt;
+    more = true;
+  }
   uint32_t used = 0;  // of this warp's ring, so far
   bool ok = true;
   uint8_t* const ring = smem + warp * D8_NB * TILE8_BYTES;
   const int page_tiles = a.v.page_size / TILE_TOKENS;
-  while (pos < hi) {
-    // ---- one segment: tiles [tile0, tile1) of group (b, kvh)
-    const int tile1 = (int)min((long long)nt, tile0 + (hi - pos));
+  auto out_row = [&](int row) {
+    return ((size_t)x.b * a.n_tok + x.tok0 + row / G) * a.n_q_heads + (size_t)kvh * G + row % G;
+  };
+  while (more) {
+    // ---- one segment: tiles [tile0, tile1) of group (e, kvh)
+    const int tile1 = uncut ? nt : (int)min((long long)nt, tile0 + (hi - pos));
     const int mine = ok && tile1 - tile0 > warp ? (tile1 - tile0 - warp + D8_WARPS - 1) / D8_WARPS : 0;  // this warp's
     auto issue = [&](int j) {  // the warp's j-th tile of the segment; whether it has a page
       const int tile = tile0 + warp + D8_WARPS * j, idx = tile / page_tiles;
       uint64_t* const bar = &bars[warp][(used + j) % D8_NB];
-      int page = b;
-      if (a.v.block_table) page = idx < a.v.max_pages ? a.v.block_table[(size_t)b * a.v.max_pages + idx] : -1;
+      int page = x.b;
+      if (a.v.block_table) page = idx < a.v.max_pages ? a.v.block_table[(size_t)x.b * a.v.max_pages + idx] : -1;
       const bool there = page >= 0 && page < a.v.n_pages;
       if (lane == 0) {
         if (there) {
@@ -135,8 +203,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     uint32_t have = 0;  // bit j mod NB: the warp's tile j has a page
     for (int j = 0; j < D8_NB && j < mine; ++j) have |= issue(j) << (j % D8_NB);
     uint32_t qa[8][4];
-    const int head = FEW ? g & 3 : g;
-    const float qs = load_q8(a.q, a.dtype, (size_t)b * a.n_q_heads + (size_t)kvh * G + head, head < G, a.scale, qa);
+    const int rows = x.n_live * G, row = FEW ? g & 3 : g;  // row: token row / G of the block, head row % G of the group
+    const float qs = load_q8(a.q, a.dtype, out_row(row), row < rows, a.scale, qa);
+    const int seen = row < rows ? x.pos0 + row / G + 1 : 0;  // keys
     Row8 r;
     row8_init(r);
     int j = 0;
@@ -146,9 +215,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       if (!ok) break;
       uint8_t* const t = ring + n % D8_NB * TILE8_BYTES;
       if ((have >> (j % D8_NB)) & 1) {
-        const int n_valid = min(TILE_TOKENS, ctx - (tile0 + warp + D8_WARPS * j) * TILE_TOKENS);
-        if (n_valid < TILE_TOKENS) clear_v_rows8(t, n_valid);
-        tile8<CODE, FEW>(t, n_valid, qa, qs, r);
+        const int at = (tile0 + warp + D8_WARPS * j) * TILE_TOKENS;
+        if (x.ctx - at < TILE_TOKENS) clear_v_rows8(t, x.ctx - at);
+        tile8<CODE, FEW>(t, seen - at, qa, qs, r);
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this slot's reads before the next copy into it
@@ -164,7 +233,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     __syncthreads();
     const bool whole = tile0 == 0 && tile1 == nt;
     const int slot = 2 * c + (pos == lo ? 0 : 1);
-    for (int h = warp; h < G; h += D8_WARPS) {
+    for (int h = warp; h < rows; h += D8_WARPS) {
       float M = -CUDART_INF_F, MO = -CUDART_INF_F;
 #pragma unroll
       for (int w = 0; w < D8_WARPS; ++w) {
@@ -181,7 +250,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
         o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y); o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
       }
       if (whole) {
-        finish_row8(a, (size_t)b * a.n_q_heads + (size_t)kvh * G + h, M, MO, L, o);
+        finish_row8(a, out_row(h), M, MO, L, o);
       } else {
         __stcg(reinterpret_cast<float4*>(a.part_o + ((size_t)slot * A8_ROWS + h) * D) + lane, o);
         if (lane == 0) __stcg(&a.part_ml[slot * A8_ROWS + h], make_float4(M, MO, L, 0.f));
@@ -201,7 +270,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const int gi = b * Hkv + kvh;
+        const size_t gi = (size_t)e * Hkv + kvh;
         const int seen = atomicAdd(&a.counters[gi], 1);
         s_last = seen == c1 - c0;
         if (seen < 0 || seen > c1 - c0) {
@@ -214,7 +283,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       if (s_last) {
         // slot of contributor k: 2 k + 1 where the group starts inside k's range, 2 k otherwise
         const int extra = g0 > c0 * total / N ? 1 : 0;
-        for (int h = warp; h < G; h += D8_WARPS) {
+        for (int h = warp; h < rows; h += D8_WARPS) {
           auto slot_of = [&](int k) { return (2 * k + (k == c0 ? extra : 0)) * A8_ROWS + h; };
           float M = -CUDART_INF_F, MO = -CUDART_INF_F, L = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -248,63 +317,99 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
               o.x = fmaf(x[i].x, f, o.x); o.y = fmaf(x[i].y, f, o.y); o.z = fmaf(x[i].z, f, o.z); o.w = fmaf(x[i].w, f, o.w);
             }
           }
-          finish_row8(a, (size_t)b * a.n_q_heads + (size_t)kvh * G + h, M, MO, L, o);
+          finish_row8(a, out_row(h), M, MO, L, o);
         }
       }
     }
     // sml, s_last and the sums are read before the next segment's copies and sums take their place
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    if (uncut) {
+      gi += gridDim.x;
+      more = take();
+      continue;
+    }
     pos += tile1 - tile0;
     tile0 = 0;
-    if (pos < hi && ++kvh == Hkv) {
+    more = pos < hi;
+    if (more && ++kvh == Hkv) {
       kvh = 0;
-      do ++b; while (clamp_ctx8(a, b) == 0);
-      ctx = clamp_ctx8(a, b);
-      nt = (ctx + TILE_TOKENS - 1) / TILE_TOKENS;
+      do x = d8_entry(a, ++e);
+      while (x.ctx == 0);
+      nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
     }
   }
 }
 
-// CTAs of a call: one per SM, fewer where that leaves warps without a tile.
-static int decode8_ctas(int batch, int n_kv_heads, int max_ctx) {
-  const long long tiles = (long long)batch * n_kv_heads * ((max_ctx + TILE_TOKENS - 1) / TILE_TOKENS);
-  return (int)std::max(1ll, std::min((long long)sm_count(), (tiles + D8_WARPS - 1) / D8_WARPS));
+// CTAs of a call over `entries` sequences or blocks: one per SM, fewer where that leaves CTAs without a group and warps
+// without a tile.
+static int decode8_ctas(long long entries, int n_kv_heads, int max_ctx) {
+  const long long groups = entries * n_kv_heads, tiles = groups * ((max_ctx + TILE_TOKENS - 1) / TILE_TOKENS);
+  return (int)std::max(1ll, std::min((long long)sm_count(), std::max(groups, (tiles + D8_WARPS - 1) / D8_WARPS)));
 }
 
-static size_t counter8_bytes(int batch, int n_kv_heads) { return ((size_t)batch * n_kv_heads * 4 + 255) & ~(size_t)255; }
+static size_t counter8_bytes(long long entries, int n_kv_heads) { return ((size_t)entries * n_kv_heads * 4 + 255) & ~(size_t)255; }
 
-size_t decode8_workspace_bytes(int batch, int n_kv_heads, int max_ctx) {
-  const size_t slots = 2 * (size_t)decode8_ctas(batch, n_kv_heads, max_ctx);
-  return counter8_bytes(batch, n_kv_heads) + slots * A8_ROWS * (sizeof(float4) + D * sizeof(float));
+static size_t workspace8_bytes(long long entries, int n_kv_heads, int max_ctx) {
+  const size_t slots = 2 * (size_t)decode8_ctas(entries, n_kv_heads, max_ctx);
+  return counter8_bytes(entries, n_kv_heads) + slots * A8_ROWS * (sizeof(float4) + D * sizeof(float));
 }
+
+static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, int dtype, void* out, void* workspace, void* stream) {
+  a.q = q;
+  a.dtype = dtype;
+  a.n_q_heads = n_q_heads;
+  a.g_real = n_q_heads / a.v.n_kv_heads;
+  a.scale = scale;
+  a.out = out;
+  const long long entries = (long long)a.batch * a.n_blk;
+  const int n = decode8_ctas(entries, a.v.n_kv_heads, a.max_ctx);
+  uint8_t* w = (uint8_t*)workspace;
+  a.counters = (int32_t*)w;
+  w += counter8_bytes(entries, a.v.n_kv_heads);
+  a.part_ml = (float4*)w;
+  a.part_o = (float*)(w + 2 * (size_t)n * A8_ROWS * sizeof(float4));
+  const bool few = a.g_real * a.tq <= 4;
+  auto fn = a.v.code == IQ_E4M3 ? (few ? decode8_kernel<IQ_E4M3, true> : decode8_kernel<IQ_E4M3, false>)
+                                : (few ? decode8_kernel<IQ_S8, true> : decode8_kernel<IQ_S8, false>);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, D8_SMEM);
+  if (e != cudaSuccess) return (int)e;
+  return (int)launch_pdl(fn, dim3(n), dim3(D8_THREADS), D8_SMEM, (cudaStream_t)stream, a);
+}
+
+size_t decode8_workspace_bytes(int batch, int n_kv_heads, int max_ctx) { return workspace8_bytes(batch, n_kv_heads, max_ctx); }
 
 int launch_decode8(const View8& v, const void* q, int dtype, int batch, int n_q_heads, const int32_t* ctx_len,
                    int max_ctx, float scale, void* out, void* workspace, void* stream) {
   if (batch == 0) return 0;
-  Decode8Args a;
+  Decode8Args a = {};
   a.v = v;
-  a.q = q;
-  a.dtype = dtype;
   a.batch = batch;
-  a.n_q_heads = n_q_heads;
-  a.g_real = n_q_heads / v.n_kv_heads;
   a.max_ctx = max_ctx;
   a.ctx_len = ctx_len;
-  a.scale = scale;
-  a.out = out;
-  const int n = decode8_ctas(batch, v.n_kv_heads, max_ctx);
-  uint8_t* w = (uint8_t*)workspace;
-  a.counters = (int32_t*)w;
-  w += counter8_bytes(batch, v.n_kv_heads);
-  a.part_ml = (float4*)w;
-  a.part_o = (float*)(w + 2 * (size_t)n * A8_ROWS * sizeof(float4));
-  const bool few = a.g_real <= 4;
-  auto fn = v.code == IQ_E4M3 ? (few ? decode8_kernel<IQ_E4M3, true> : decode8_kernel<IQ_E4M3, false>)
-                              : (few ? decode8_kernel<IQ_S8, true> : decode8_kernel<IQ_S8, false>);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, D8_SMEM);
+  a.n_tok = a.tq = a.n_blk = 1;
+  return launch8(a, n_q_heads, scale, q, dtype, out, workspace, stream);
+}
+
+// A chunk of query tokens, up to eight rows (tokens x heads) a block: float32 queries, whose products take two terms.
+size_t chunk8_workspace_bytes(int batch, int n_tok, int g, int n_kv_heads, int max_ctx) {
+  return workspace8_bytes((long long)batch * ((n_tok + A8_ROWS / g - 1) / (A8_ROWS / g)), n_kv_heads, max_ctx);
+}
+int launch_chunk8(const View8& v, const void* q, int dtype, int batch, int n_tok, int n_q_heads, const int32_t* start,
+                  const int32_t* n_valid, int max_ctx, float scale, void* out, void* workspace, void* stream) {
+  Decode8Args a = {};
+  a.v = v;
+  a.batch = batch;
+  a.max_ctx = max_ctx;
+  a.n_tok = n_tok;
+  a.tq = A8_ROWS / (n_q_heads / v.n_kv_heads);
+  a.n_blk = (n_tok + a.tq - 1) / a.tq;
+  a.start = start;
+  a.n_valid = n_valid;
+  // (this workspace comes as it is)
+  const cudaError_t e = cudaMemsetAsync(workspace, 0, counter8_bytes((long long)batch * a.n_blk, v.n_kv_heads), (cudaStream_t)stream);
   if (e != cudaSuccess) return (int)e;
-  return (int)launch_pdl(fn, dim3(n), dim3(D8_THREADS), D8_SMEM, (cudaStream_t)stream, a);
+  return launch8(a, n_q_heads, scale, q, dtype, out, workspace, stream);
 }
 
 }  // namespace iq

@@ -318,22 +318,30 @@ __global__ void __launch_bounds__(PG_THREADS) pages_copy_plan_kernel(iq_pages p,
   if (threadIdx.x == 0) w.count[0] = n;
 }
 
-// The lists' pages in every layer of one pool: a warp per (entry, layer, head) run of whole tile records.
+// The lists' pages in every layer of one pool.  An (entry, layer, head) run of whole tile records is cut into pieces of
+// 4 KB, a warp's eight loads of 512 bytes each, all in flight before the first store.  Pages of 8224-byte records, 135 MB
+// moved: PLACEHOLDER_MOVE (a run of 16 KB a warp, four loads at a time: 58 us).
+constexpr int MOVE_PIECE = 256;  // 16-byte words
 __global__ void __launch_bounds__(256) pages_move_kernel(uint8_t* pool, int n_layers, int n_heads, int tile_bytes,
                                                          int page_tiles, int n_pages, PagesWs w) {
-  const int lane = threadIdx.x & 31;
-  const long long items = (long long)w.count[0] * n_layers * n_heads;
-  const size_t run = (size_t)page_tiles * tile_bytes;
+  const int lane = threadIdx.x & 31, words = page_tiles * (tile_bytes / 16), pieces = (words + MOVE_PIECE - 1) / MOVE_PIECE;
+  const long long items = (long long)w.count[0] * n_layers * n_heads * pieces;
   for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; i < items; i += (long long)gridDim.x * 8) {
-    const int head = (int)(i % n_heads), layer = (int)(i / n_heads % n_layers), e = (int)(i / n_heads / n_layers);
-    const int tiles = w.tiles[e];
-    if (!tiles) continue;
+    const int piece = (int)(i % pieces);
+    const long long j = i / pieces;
+    const int head = (int)(j % n_heads), layer = (int)(j / n_heads % n_layers), e = (int)(j / n_heads / n_layers);
+    const int n = w.tiles[e] * (tile_bytes / 16), at = piece * MOVE_PIECE + lane;
+    if (piece * MOVE_PIECE >= n) continue;
     const size_t base = (size_t)layer * n_pages;
-    const uint4* s = reinterpret_cast<const uint4*>(pool + ((base + w.src[e]) * n_heads + head) * run);
-    uint4* d = reinterpret_cast<uint4*>(pool + ((base + w.dst[e]) * n_heads + head) * run);
-    const int n = tiles * tile_bytes / 16;
-#pragma unroll 4
-    for (int k = lane; k < n; k += 32) d[k] = s[k];
+    const uint4* s = reinterpret_cast<const uint4*>(pool) + ((base + w.src[e]) * n_heads + head) * words + at;
+    uint4* d = reinterpret_cast<uint4*>(pool) + ((base + w.dst[e]) * n_heads + head) * words + at;
+    uint4 x[MOVE_PIECE / 32];
+#pragma unroll
+    for (int k = 0; k < MOVE_PIECE / 32; ++k)
+      if (at + 32 * k < n) x[k] = __ldcs(s + 32 * k);
+#pragma unroll
+    for (int k = 0; k < MOVE_PIECE / 32; ++k)
+      if (at + 32 * k < n) __stcs(d + 32 * k, x[k]);
   }
 }
 
