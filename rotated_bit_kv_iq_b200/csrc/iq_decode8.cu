@@ -25,7 +25,7 @@ struct Decode8Args {
   View8 v;
   const void* q;
   int dtype, batch, n_q_heads, g_real, max_ctx;
-  const int32_t* ctx_len;  // decode; or, with ctx_len NULL, blocks of tq of a chunk's n_tok tokens, n_blk a sequence:
+  const int32_t* ctx_len;  // decode; or (CHUNK, ctx_len NULL) blocks of tq of a chunk's n_tok tokens, n_blk a sequence:
   int n_tok, tq, n_blk;
   const int32_t* start;
   const int32_t* n_valid;
@@ -40,9 +40,10 @@ struct Decode8Args {
 struct D8Entry {
   int b, tok0, n_live, pos0, ctx;  // its tokens, the first one's position, the keys that the last one sees
 };
+template <bool CHUNK>
 __device__ __forceinline__ D8Entry d8_entry(const Decode8Args& a, int e) {
   D8Entry x;
-  if (a.ctx_len) {
+  if (!CHUNK) {
     const int c = a.ctx_len[e];
     x.b = e;
     x.tok0 = 0;
@@ -59,7 +60,10 @@ __device__ __forceinline__ D8Entry d8_entry(const Decode8Args& a, int e) {
   }
   return x;
 }
-__device__ __forceinline__ int d8_tiles(const Decode8Args& a, int e) { return (d8_entry(a, e).ctx + TILE_TOKENS - 1) / TILE_TOKENS; }
+template <bool CHUNK>
+__device__ __forceinline__ int d8_tiles(const Decode8Args& a, int e) {
+  return (d8_entry<CHUNK>(a, e).ctx + TILE_TOKENS - 1) / TILE_TOKENS;
+}
 
 // Final value of one row of the group: lane holds sums of coordinates 4 lane ..
 __device__ __forceinline__ void finish_row8(const Decode8Args& a, size_t row, float M, float MO, float L, float4 o) {
@@ -67,7 +71,7 @@ __device__ __forceinline__ void finish_row8(const Decode8Args& a, size_t row, fl
   store4(a.out, a.dtype, row * D + 4 * (threadIdx.x & 31), make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
 }
 
-template <int CODE, bool FEW>
+template <int CODE, bool FEW, bool CHUNK>
 __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[D8_WARPS][D8_NB];
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   long long mine = 0;
   int most = 0;  // tiles of an entry
   for (int e = e0; e < e1; ++e) {
-    const int n = d8_tiles(a, e);
+    const int n = d8_tiles<CHUNK>(a, e);
     mine += n;
     most = max(most, n);
   }
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   const long long lo = c < N ? c * total / N : total, hi = c < N ? (c + 1) * total / N : total;
   long long acc = before;  // tiles of all groups before entry e
   for (int e = e0; e < e1 && acc <= lo; ++e) {
-    const long long n = (long long)Hkv * d8_tiles(a, e);
+    const long long n = (long long)Hkv * d8_tiles<CHUNK>(a, e);
     if (lo < hi && lo < acc + n) {
       s_start[0] = e;
       s_start[1] = (int)(lo - acc);
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   if (c == 0 && a.v.status)  // lengths, counts and starts outside their ranges
     for (int b = tid; b < a.batch; b += D8_THREADS) {
       bool bad;
-      if (a.ctx_len) {
+      if (!CHUNK) {
         bad = a.ctx_len[b] < 0 || a.ctx_len[b] > a.max_ctx;
       } else {
         const int cnt = a.n_valid ? a.n_valid[b] : a.n_tok, st = a.start[b];
@@ -137,9 +141,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       if (bad) atomicOr(a.v.status, IQ_DEVERR_CTX);
     }
   // sequences with nothing to see: zero rows
-  if (a.ctx_len)
+  if (!CHUNK)
     for (int b = c; b < a.batch; b += gridDim.x)
-      if (d8_entry(a, b).ctx == 0)
+      if (d8_entry<CHUNK>(a, b).ctx == 0)
         for (int i = tid; i < a.n_q_heads * (D / 4); i += D8_THREADS)
           store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   __syncthreads();
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     for (; gi < (long long)E * Hkv; gi += gridDim.x) {
       e = (int)(gi / Hkv);
       kvh = (int)(gi % Hkv);
-      x = d8_entry(a, e);
+      x = d8_entry<CHUNK>(a, e);
       nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
       if (nt) return true;
     }
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     more = take();
   } else {
     e = s_start[0];
-    x = d8_entry(a, e);
+    x = d8_entry<CHUNK>(a, e);
     nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
     kvh = s_start[1] / nt;
     tile0 = s_start[1] % nt;
@@ -176,7 +180,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   uint8_t* const ring = smem + warp * D8_NB * TILE8_BYTES;
   const int page_tiles = a.v.page_size / TILE_TOKENS;
   auto out_row = [&](int row) {
-    return ((size_t)x.b * a.n_tok + x.tok0 + row / G) * a.n_q_heads + (size_t)kvh * G + row % G;
+    return CHUNK ? ((size_t)x.b * a.n_tok + x.tok0 + row / G) * a.n_q_heads + (size_t)kvh * G + row % G
+                 : (size_t)x.b * a.n_q_heads + (size_t)kvh * G + row;
   };
   while (more) {
     // ---- one segment: tiles [tile0, tile1) of group (e, kvh)
@@ -203,9 +208,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     uint32_t have = 0;  // bit j mod NB: the warp's tile j has a page
     for (int j = 0; j < D8_NB && j < mine; ++j) have |= issue(j) << (j % D8_NB);
     uint32_t qa[8][4];
-    const int rows = x.n_live * G, row = FEW ? g & 3 : g;  // row: token row / G of the block, head row % G of the group
+    const int rows = CHUNK ? x.n_live * G : G, row = FEW ? g & 3 : g;  // row: token row / G of the block, head row % G of the group
     const float qs = load_q8(a.q, a.dtype, out_row(row), row < rows, a.scale, qa);
-    const int seen = row < rows ? x.pos0 + row / G + 1 : 0;  // keys
+    const int seen = !CHUNK ? x.ctx : row < rows ? x.pos0 + row / G + 1 : 0;  // keys
     Row8 r;
     row8_init(r);
     int j = 0;
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     more = pos < hi;
     if (more && ++kvh == Hkv) {
       kvh = 0;
-      do x = d8_entry(a, ++e);
+      do x = d8_entry<CHUNK>(a, ++e);
       while (x.ctx == 0);
       nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
     }
@@ -369,9 +374,11 @@ static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, in
   w += counter8_bytes(entries, a.v.n_kv_heads);
   a.part_ml = (float4*)w;
   a.part_o = (float*)(w + 2 * (size_t)n * A8_ROWS * sizeof(float4));
-  const bool few = a.g_real * a.tq <= 4;
-  auto fn = a.v.code == IQ_E4M3 ? (few ? decode8_kernel<IQ_E4M3, true> : decode8_kernel<IQ_E4M3, false>)
-                                : (few ? decode8_kernel<IQ_S8, true> : decode8_kernel<IQ_S8, false>);
+  const bool few = a.g_real * a.tq <= 4, e4 = a.v.code == IQ_E4M3;
+  auto fn = a.ctx_len ? (few ? (e4 ? decode8_kernel<IQ_E4M3, true, false> : decode8_kernel<IQ_S8, true, false>)
+                             : (e4 ? decode8_kernel<IQ_E4M3, false, false> : decode8_kernel<IQ_S8, false, false>))
+                      : (few ? (e4 ? decode8_kernel<IQ_E4M3, true, true> : decode8_kernel<IQ_S8, true, true>)
+                             : (e4 ? decode8_kernel<IQ_E4M3, false, true> : decode8_kernel<IQ_S8, false, true>));
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, D8_SMEM);
   if (e != cudaSuccess) return (int)e;
   return (int)launch_pdl(fn, dim3(n), dim3(D8_THREADS), D8_SMEM, (cudaStream_t)stream, a);

@@ -98,6 +98,7 @@ __device__ __forceinline__ bool listed_before(const int* ids, int i, int id) {
 
 __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(iq_pages p, const int32_t* __restrict__ ids,
                                                                   const int32_t* __restrict__ new_len, int n, PagesWs w) {
+  pdl_wait();
   __shared__ int s_id[IQ_PAGES_MAX_LIST];
   __shared__ int s_need[IQ_PAGES_MAX_LIST];
   __shared__ int scratch[PG_WARPS + 1];
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(iq_pages p, co
 
 // One CTA per entry.
 __global__ void __launch_bounds__(128) pages_free_kernel(iq_pages p, const int32_t* __restrict__ ids) {
+  pdl_wait();
   const int i = blockIdx.x, id = ids[i];
   bool bad = id < 0 || id >= p.max_seqs;
   for (int j = threadIdx.x; j < i; j += 128) bad |= ids[j] == id;
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(128) pages_free_kernel(iq_pages p, const int32
 
 __global__ void __launch_bounds__(PG_THREADS) pages_fork_kernel(iq_pages p, const int32_t* __restrict__ parent,
                                                                 const int32_t* __restrict__ child, int n, PagesWs w) {
+  pdl_wait();
   __shared__ int s_child[IQ_PAGES_MAX_LIST];
   __shared__ int s_len[IQ_PAGES_MAX_LIST];  // the parent's length; -1: refused
   __shared__ int scratch[PG_WARPS + 1];
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_fork_kernel(iq_pages p, cons
 }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(iq_pages p, int32_t* n_held, PagesWs w) {
+  pdl_wait();
   __shared__ int scratch[PG_WARPS + 1];
   int32_t* const ref = p.ref_dev;
   const int held = rank_pages(p.n_pages, scratch, [&](int g) { return ref[g] > 0; }, [](int, int) {});
@@ -288,6 +292,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(iq_pages p, i
 
 // The tables after a compaction: an entry at or above the number of held pages has moved.
 __global__ void __launch_bounds__(256) pages_remap_kernel(iq_pages p, PagesWs w) {
+  pdl_wait();
   const size_t n = (size_t)p.max_seqs * p.max_pages_per_seq;
   const int held = w.count[1];
   if (w.count[0] == 0) return;
@@ -299,6 +304,7 @@ __global__ void __launch_bounds__(256) pages_remap_kernel(iq_pages p, PagesWs w)
 
 __global__ void __launch_bounds__(PG_THREADS) pages_copy_plan_kernel(iq_pages p, const int32_t* __restrict__ src,
                                                                      const int32_t* __restrict__ dst, int n, PagesWs w) {
+  pdl_wait();
   __shared__ int s_src[IQ_PAGES_MAX_LIST];
   __shared__ int s_dst[IQ_PAGES_MAX_LIST];
   for (int i = threadIdx.x; i < n; i += PG_THREADS) {
@@ -324,6 +330,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_copy_plan_kernel(iq_pages p,
 constexpr int MOVE_PIECE = 256;  // 16-byte words
 __global__ void __launch_bounds__(256) pages_move_kernel(uint8_t* pool, int n_layers, int n_heads, int tile_bytes,
                                                          int page_tiles, int n_pages, PagesWs w) {
+  pdl_wait();
   const int lane = threadIdx.x & 31, words = page_tiles * (tile_bytes / 16), pieces = (words + MOVE_PIECE - 1) / MOVE_PIECE;
   const long long items = (long long)w.count[0] * n_layers * n_heads * pieces;
   for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5; i < items; i += (long long)gridDim.x * 8) {
@@ -345,13 +352,14 @@ __global__ void __launch_bounds__(256) pages_move_kernel(uint8_t* pool, int n_la
   }
 }
 
-// Nothing: what follows it on the stream starts after the kernels before it are complete.
+// Nothing: launched plainly, it starts once the kernels before it are complete, so that what follows it on the stream may
+// start early.
 __global__ void pages_end_kernel() {}
 
 static int finish(const iq_pages& p, const PagePools& pools, const PagesWs& w, cudaStream_t st) {
   for (int i = 0; i < pools.n; ++i)
-    pages_move_kernel<<<sm_count() * 8, 256, 0, st>>>(pools.base[i], pools.n_layers[i], pools.n_kv_heads[i],
-                                                      pools.tile_bytes[i], p.page_size / TILE_TOKENS, p.n_pages, w);
+    launch_pdl(pages_move_kernel, dim3(sm_count() * 8), dim3(256), 0, st, pools.base[i], pools.n_layers[i],
+               pools.n_kv_heads[i], pools.tile_bytes[i], (int)(p.page_size / TILE_TOKENS), (int)p.n_pages, w);
   pages_end_kernel<<<1, 32, 0, st>>>();
   return (int)cudaGetLastError();
 }
@@ -359,14 +367,14 @@ static int finish(const iq_pages& p, const PagePools& pools, const PagesWs& w, c
 int launch_pages_extend(const iq_pages& p, const int32_t* ids, const int32_t* len, int n, void* ws, void* stream) {
   if (n == 0) return 0;
   const cudaStream_t st = (cudaStream_t)stream;
-  pages_extend_kernel<<<1, PG_THREADS, 0, st>>>(p, ids, len, n, carve(p, ws));
+  launch_pdl(pages_extend_kernel, dim3(1), dim3(PG_THREADS), 0, st, p, ids, len, n, carve(p, ws));
   pages_end_kernel<<<1, 32, 0, st>>>();
   return (int)cudaGetLastError();
 }
 int launch_pages_free(const iq_pages& p, const int32_t* ids, int n, void* stream) {
   if (n == 0) return 0;
   const cudaStream_t st = (cudaStream_t)stream;
-  pages_free_kernel<<<n, 128, 0, st>>>(p, ids);
+  launch_pdl(pages_free_kernel, dim3(n), dim3(128), 0, st, p, ids);
   pages_end_kernel<<<1, 32, 0, st>>>();
   return (int)cudaGetLastError();
 }
@@ -374,22 +382,22 @@ int launch_pages_fork(const iq_pages& p, const PagePools& pools, const int32_t* 
                       void* ws, void* stream) {
   if (n == 0) return 0;
   const PagesWs w = carve(p, ws);
-  pages_fork_kernel<<<1, PG_THREADS, 0, (cudaStream_t)stream>>>(p, parent, child, n, w);
+  launch_pdl(pages_fork_kernel, dim3(1), dim3(PG_THREADS), 0, (cudaStream_t)stream, p, parent, child, n, w);
   return finish(p, pools, w, (cudaStream_t)stream);
 }
 int launch_pages_compact(const iq_pages& p, const PagePools& pools, int32_t* n_held, void* ws, void* stream) {
   const PagesWs w = carve(p, ws);
   const cudaStream_t st = (cudaStream_t)stream;
-  pages_compact_kernel<<<1, PG_THREADS, 0, st>>>(p, n_held, w);
+  launch_pdl(pages_compact_kernel, dim3(1), dim3(PG_THREADS), 0, st, p, n_held, w);
   const size_t entries = (size_t)p.max_seqs * p.max_pages_per_seq;
-  pages_remap_kernel<<<(unsigned)std::min<size_t>((entries + 255) / 256, (size_t)sm_count() * 8), 256, 0, st>>>(p, w);
+  launch_pdl(pages_remap_kernel, dim3((unsigned)std::min<size_t>((entries + 255) / 256, (size_t)sm_count() * 8)), dim3(256), 0, st, p, w);
   return finish(p, pools, w, st);
 }
 int launch_pages_copy(const iq_pages& p, const PagePools& pools, const int32_t* src, const int32_t* dst, int n,
                       void* ws, void* stream) {
   if (n == 0) return 0;
   const PagesWs w = carve(p, ws);
-  pages_copy_plan_kernel<<<1, PG_THREADS, 0, (cudaStream_t)stream>>>(p, src, dst, n, w);
+  launch_pdl(pages_copy_plan_kernel, dim3(1), dim3(PG_THREADS), 0, (cudaStream_t)stream, p, src, dst, n, w);
   return finish(p, pools, w, (cudaStream_t)stream);
 }
 
