@@ -41,15 +41,16 @@ __device__ __forceinline__ float scale_for(uint32_t amax) {
 
 // Codes of eight values as two words; NaN -> 0, saturating.
 //   e4m3: the product with a power of two is exact, the conversion the one rounding.
-//   int8: k = nearest integer to x * (1 / s) is the nearest to x / s or next to it, and d = x - k s is exact (s has 8
-//   significant bits, k 7), so that |d| against s / 2 says which; a tie goes to the even one.  (A division for each value
-//   took 90 us for the 32K prompt, this 59.)
-template <int CODE>
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv, bool odd_values) {
+//   int8: q = x (1 / s), its remainder x - q s and q + remainder (1 / s), each rounded once, give the correctly rounded
+//   quotient (Markstein, 1990: 1 / s correctly rounded, q within one unit in the last place); adding 1.5 2^23 rounds that
+//   to the nearest integer, ties to even, in the low byte.  (The compiler's division for each value: 90 us for the 32K
+//   prompt; the nearest integer to x (1 / s) and a branch for ties: 57; this: 53.)
+template <int CODE, bool ODD>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv) {
   float y[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) y[k] = x[k];
-  if (odd_values) {  // NaN or infinities among the tile's values
+  if (ODD) {  // NaN or infinities among the tile's values
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float top = CODE == IQ_E4M3 ? 448.f : 127.f;
@@ -66,20 +67,10 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, flo
           : "f"(y[4 * h] * inv), "f"(y[4 * h + 1] * inv), "f"(y[4 * h + 2] * inv), "f"(y[4 * h + 3] * inv));
   } else {
     uint32_t c[8];
-    float far = 0.f, d[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float t = fmaf(y[k], inv, kMagicF);  // the integer in the low bits
-      c[k] = __float_as_uint(t);
-      d[k] = fmaf(-(t - kMagicF), scale, y[k]);
-      far = fmaxf(far, fabsf(d[k]));
-    }
-    if (far * 2.f >= scale) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float e = fabsf(d[k]) * 2.f;
-        if (e > scale || (e == scale && (c[k] & 1u))) c[k] += d[k] > 0.f ? 1u : 0xFFFFFFFFu;
-      }
+      const float q = __fmul_rn(y[k], inv);
+      c[k] = round_low_bits(__fmaf_rn(__fmaf_rn(-q, scale, y[k]), inv, q));
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -95,20 +86,19 @@ __device__ __forceinline__ void load8(const T* p, float f[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void widen8(uint4 u, float f[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      f[2 * i] = a.x;
-      f[2 * i + 1] = a.y;
-    } else {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = a.x;
+        f[2 * i + 1] = a.y;
+      } else {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
     }
   }
 }
@@ -152,36 +142,36 @@ __global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) 
   const int lo = (int)(first - t0), hi = (int)(end - t0);  // the new tokens' rows
   const T* const src = x + ((long long)b * a.n_new + (t0 - start)) * stride + head * D + 8 * c8;
 
-  // the largest magnitude (16-bit types: as their bit patterns, two at a time), and the rows themselves where they fit
-  // the registers
-  constexpr bool KEEP = sizeof(T) == 2;
-  uint4 raw[KEEP ? 16 : 1];
+  // Two passes over the rows, the second from L1 (the rows in registers: 104 of them, code without loops, and 59 us for the
+  // 32K prompt).  First the largest magnitude, of 16-bit types two at a time.
+  constexpr bool WIDE = sizeof(T) == 4;
   uint32_t amax = 0;
   bool odd_values = false;  // a NaN or an infinity
-  if constexpr (KEEP) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + odd;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (r >= lo && r < hi) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
-    }
+  if constexpr (!WIDE) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    auto larger = [](uint32_t x, uint32_t y) {  // of two pairs of magnitudes; NaN wins
+      const T2 z = __hmax2_nan(*reinterpret_cast<const T2*>(&x), *reinterpret_cast<const T2*>(&y));
+      return *reinterpret_cast<const uint32_t*>(&z);
+    };
     uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu), __vmaxu2(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu)));
+#pragma unroll 8
+    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
+      if (r < lo) continue;
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
+      m = larger(m, larger(larger(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), larger(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
+    }
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
     constexpr bool half = std::is_same<T, __half>::value;
     odd_values = m >= (half ? 0x7C00u : 0x7F80u);
     amax = half ? __float_as_uint(__half2float(__ushort_as_half((uint16_t)m))) : m << 16;
   }
-  if (!KEEP || odd_values) {
+  if (WIDE || odd_values) {
     amax = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = 2 * i + odd;
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if constexpr (KEEP) widen8<T>(raw[i], f);
-      else if (r >= lo && r < hi) load8(src + r * stride, f);
+#pragma unroll 4
+    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
+      if (r < lo) continue;
+      float f[8];
+      load8(src + r * stride, f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         odd_values |= !(fabsf(f[k]) < CUDART_INF_F);
@@ -213,18 +203,20 @@ __global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) 
         f[2 * k] = g.x * was;
         f[2 * k + 1] = g.y * was;
       }
-      *p = quantise8<CODE>(f, scale, inv, true);  // (slots that held nothing may be NaN codes)
+      *p = quantise8<CODE, true>(f, scale, inv);  // (slots that held nothing may be NaN codes)
     }
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 2 * i + odd;
-    if (r < lo || r >= hi) continue;
-    float f[8];
-    if constexpr (KEEP) widen8<T>(raw[i], f);
-    else load8(src + r * stride, f);
-    *reinterpret_cast<uint2*>(rows + chunk8(r, c8 >> 1) + 8 * (c8 & 1)) = quantise8<CODE>(f, scale, inv, odd_values);
-  }
+  auto write = [&](auto odd_c) {
+#pragma unroll 4
+    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
+      if (r < lo) continue;
+      float f[8];
+      load8(src + r * stride, f);
+      *reinterpret_cast<uint2*>(rows + chunk8(r, c8 >> 1) + 8 * (c8 & 1)) = quantise8<CODE, decltype(odd_c)::value>(f, scale, inv);
+    }
+  };
+  if (odd_values) write(std::true_type());
+  else write(std::false_type());
 }
 
 int launch_append8(const View8& v, const void* k, const void* vsrc, int dtype, long long ks, long long vs, int batch, int n_new,

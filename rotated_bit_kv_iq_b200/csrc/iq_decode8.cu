@@ -5,7 +5,7 @@
 // a block of its query tokens; CTA c of N takes tiles
 // [c T / N, (c + 1) T / N), whatever the mix of lengths.  Its warps take the tiles of each group's segment in turn, each
 // through a ring of its own of two bulk-copied tile records: twelve warps, three a scheduler, at 168 registers.  On the
-// 16-sequence layer: PLACEHOLDER_SERVE us, 105 with eight warps (197 registers); 121 with sixteen (128 registers, which
+// 16-sequence layer: 92-96 us, 105 with eight warps (197 registers); 121 with sixteen (128 registers, which
 // do not hold a tile's work) on one ring of 26 records.  A segment that is a whole group is finished at once; the others
 // leave a partial (m, mo, l, O), and the last CTA of a group to arrive merges the group's partials in a fixed order, so
 // that results do not depend on who is last.  Bound by memory: 257 B for each (token, kv head).
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
           store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   __syncthreads();
   // Short groups, of two rounds of the warps at the most, are not cut: CTA c takes groups c, c + grid, ... whole, and there
-  // is nothing to merge (a 512-token layer of two kv heads: PLACEHOLDER_SHORT).
+  // is nothing to merge (a 512-token layer of two kv heads: 9 us a call, 15 cut).
   const bool uncut = most <= 2 * D8_WARPS;
   if (!uncut && lo >= hi) return;
   int e = 0, kvh = 0, nt = 0, tile0 = 0;

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_copy_plan_kernel(iq_pages p,
 
 // The lists' pages in every layer of one pool.  An (entry, layer, head) run of whole tile records is cut into pieces of
 // 4 KB, a warp's eight loads of 512 bytes each, all in flight before the first store.  Pages of 8224-byte records, 135 MB
-// moved: PLACEHOLDER_MOVE (a run of 16 KB a warp, four loads at a time: 58 us).
+// moved: 45 us (a run of 16 KB a warp, four loads at a time: 58 us).
 constexpr int MOVE_PIECE = 256;  // 16-byte words
 __global__ void __launch_bounds__(256) pages_move_kernel(uint8_t* pool, int n_layers, int n_heads, int tile_bytes,
                                                          int page_tiles, int n_pages, PagesWs w) {
