@@ -1,23 +1,29 @@
 // Causal attention of a chunk of 16-bit query tokens over the 8-bit cache on the 5th-generation tensor cores.
 //
-// A block is 256 query rows (256 / G tokens x the G heads of one kv head) as two tiles of 128; it streams the
-// keys in steps of 128 (four tile records).  8-bit codes are exact in binary16, so a step's K and V are expanded
-// once for both tiles into shared memory, and with S in tensor memory:
-//   S = Q K^T       128 x 128 x 128, Q and K in shared memory (both along the coordinates)
-//   O += P V        128 x 128 x 128, P in tensor memory (binary16, over S's own columns), V in shared memory
-//                   as it lies in the cache: rows of coordinates (N-major operand)
-// The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and
-// the V scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is a running maximum
-// of s + log2 v that follows only once it has been passed by 2^8: O is then rescaled in tensor memory, rarely.
-// p' is one binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are
-// float32.
+// A block is 256 query rows (256 / G tokens x the G heads of one kv head) as two tiles of 128; it streams the keys in steps
+// of 128 (four tile records).  8-bit codes are exact in binary16, so a step's K and V are expanded once for both tiles into
+// shared memory, and with S in tensor memory, in half-steps of 64 keys:
+//   S = Q K^T       128 x 64 x 128, Q and K in shared memory (both along the coordinates)
+//   O += P V        128 x 128 x 64, P in tensor memory (binary16, over S's own columns), V in shared memory as it lies in
+//                   the cache: rows of coordinates (N-major operand)
+// Each tile has two S buffers: while the softmax is at one half-step's scores the tensor core adds the P of the half-step
+// before and makes the scores of the one after.  (One buffer of 128 keys a tile: 318 us on the 2048-token chunk.)
+// The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and the V
+// scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is a running maximum of
+// s + log2 v that follows only once it has been passed by 2^8: O is then rescaled in tensor memory, rarely.  p' is one
+// binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are float32.
 //
-// Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that
-// neither causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block
-// cut by a run's end leaves partials, which a second kernel merges in order.
+// Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that neither
+// causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block cut by a run's
+// end leaves partials, which a second kernel merges in order.
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
-// issues the MMAs, 17 finds the records:
-// while one tile's scores are in the softmax, the tensor core works for the other tile.
+// issues the MMAs, 17 finds the records and their scales.
+//
+// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 296 us, 813 TFLOP/s, 49% of cuBLAS's bf16 rate.  Per
+// step of 5,200 cycles a CTA's MMAs take 2,500 (the 64-key score products reach 63% of the MMA rate, being fed from shared
+// memory on both sides; the P V products all of it); the softmax warps, alone on their schedulers, 2,900, bound by the
+// exponentials (MUFU); with the expansion's two warps beside them on each scheduler (14% of the time) and the hand-overs
+// the two overlap to less than half.
 #pragma once
 #include <algorithm>
 
@@ -30,8 +36,9 @@ constexpr int PT_TILE = 128;  // rows of a tile: the MMA's M
 constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
 constexpr int PT_THREADS = 640;
-// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96
-constexpr int PT_REG_SOFTMAX = 136, PT_REG_EXPAND = 72, PT_REG_MMA = 64;
+// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96.  With 64
+// for the MMA warp, which then spills, the 2048-token chunk takes 303 us instead of 296.
+constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
 constexpr float PT_SLACK = 8.f;
