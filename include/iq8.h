@@ -76,8 +76,9 @@ iq_status iq_append8(const iq_cache8* cache, int32_t layer, const void* k_dev, c
                      int64_t k_stride, int64_t v_stride, int32_t batch, int32_t n_new, const int32_t* start_pos_dev,
                      const int32_t* n_valid_dev, iq_stream_t stream);
 
-/* Workspace bytes of iq_decode8_attention on the current device (counters and split partials);
- * zero-filled before its first use, left ready for the next call, as iq_decode_workspace_size's. */
+/* Workspace bytes of iq_decode8_attention on the current device (split partials and counters);
+ * zero-filled before its first use, left ready for the next call, as iq_decode_workspace_size's.  One that
+ * is large enough for calls of several sizes serves them all in turn; other calls' scratch must not share it. */
 size_t iq_decode8_workspace_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t max_ctx);
 
 /* Decode attention over the 8-bit cache of layer `layer`: out[b][h] = sum_t softmax_t(scale <q, K_t>) V_t

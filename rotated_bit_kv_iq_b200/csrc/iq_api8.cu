@@ -129,7 +129,7 @@ iq_status iq_append8(const iq_cache8* cache, int32_t layer, const void* k_dev, c
 
 size_t iq_decode8_workspace_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_heads, int32_t max_ctx) {
   if (batch < 0 || n_q_heads < 0 || n_kv_heads < 1 || max_ctx < 0) return 0;
-  return decode8_workspace_bytes(batch, n_kv_heads, max_ctx);
+  return decode8_workspace_bytes(batch, n_kv_heads);
 }
 
 iq_status iq_decode8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,
@@ -143,7 +143,7 @@ iq_status iq_decode8_attention(const iq_cache8* cache, int32_t layer, const void
   if (!cache->block_table_dev && batch > cache->n_pages) return IQ_ERR_CAPACITY;
   if ((int64_t)max_ctx > capacity8(cache)) return IQ_ERR_CAPACITY;
   if (!aligned_to(q_dev, 16) || !aligned_to(out_dev, 16) || !aligned_to(ctx_len_dev, 4)) return IQ_ERR_ALIGNMENT;
-  IQ_TRY(check_ws(workspace_dev, workspace_bytes, decode8_workspace_bytes(batch, cache->n_kv_heads, max_ctx)));
+  IQ_TRY(check_ws(workspace_dev, workspace_bytes, decode8_workspace_bytes(batch, cache->n_kv_heads)));
   return result(launch_decode8(view8(cache, layer), q_dev, dtype, batch, n_q_heads, ctx_len_dev, max_ctx, scale, out_dev,
                                workspace_dev, stream));
 }

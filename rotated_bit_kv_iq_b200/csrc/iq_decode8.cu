@@ -32,8 +32,8 @@ struct Decode8Args {
   float scale;
   void* out;
   int32_t* counters;  // [batch * n_blk * Hkv], zero between calls
-  float4* part_ml;    // [2 N][8]: m, mo, l
-  float* part_o;      // [2 N][8][128]
+  float4* part_ml;    // [2 SMs][8]: m, mo, l
+  float* part_o;      // [2 SMs][8][128]
 };
 
 // Entry e: a sequence (decode), or a block of a sequence's query tokens.
@@ -355,10 +355,11 @@ static int decode8_ctas(long long entries, int n_kv_heads, int max_ctx) {
 
 static size_t counter8_bytes(long long entries, int n_kv_heads) { return ((size_t)entries * n_kv_heads * 4 + 255) & ~(size_t)255; }
 
-static size_t workspace8_bytes(long long entries, int n_kv_heads, int max_ctx) {
-  const size_t slots = 2 * (size_t)decode8_ctas(entries, n_kv_heads, max_ctx);
-  return counter8_bytes(entries, n_kv_heads) + slots * A8_ROWS * (sizeof(float4) + D * sizeof(float));
-}
+// Workspace: partials of a CTA on every SM, then the counters: at one place for calls of all sizes, so that none writes
+// its partials over the counters of another.
+static size_t part8_slots() { return 2 * (size_t)sm_count(); }
+static size_t part8_bytes() { return part8_slots() * A8_ROWS * (sizeof(float4) + D * sizeof(float)); }
+static size_t workspace8_bytes(long long entries, int n_kv_heads) { return part8_bytes() + counter8_bytes(entries, n_kv_heads); }
 
 static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, int dtype, void* out, void* workspace, void* stream) {
   a.q = q;
@@ -369,11 +370,9 @@ static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, in
   a.out = out;
   const long long entries = (long long)a.batch * a.n_blk;
   const int n = decode8_ctas(entries, a.v.n_kv_heads, a.max_ctx);
-  uint8_t* w = (uint8_t*)workspace;
-  a.counters = (int32_t*)w;
-  w += counter8_bytes(entries, a.v.n_kv_heads);
-  a.part_ml = (float4*)w;
-  a.part_o = (float*)(w + 2 * (size_t)n * A8_ROWS * sizeof(float4));
+  a.part_ml = (float4*)workspace;
+  a.part_o = (float*)(a.part_ml + part8_slots() * A8_ROWS);
+  a.counters = (int32_t*)((uint8_t*)workspace + part8_bytes());
   const bool few = a.g_real * a.tq <= 4, e4 = a.v.code == IQ_E4M3;
   auto fn = a.ctx_len ? (few ? (e4 ? decode8_kernel<IQ_E4M3, true, false> : decode8_kernel<IQ_S8, true, false>)
                              : (e4 ? decode8_kernel<IQ_E4M3, false, false> : decode8_kernel<IQ_S8, false, false>))
@@ -384,7 +383,7 @@ static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, in
   return (int)launch_pdl(fn, dim3(n), dim3(D8_THREADS), D8_SMEM, (cudaStream_t)stream, a);
 }
 
-size_t decode8_workspace_bytes(int batch, int n_kv_heads, int max_ctx) { return workspace8_bytes(batch, n_kv_heads, max_ctx); }
+size_t decode8_workspace_bytes(int batch, int n_kv_heads) { return workspace8_bytes(batch, n_kv_heads); }
 
 int launch_decode8(const View8& v, const void* q, int dtype, int batch, int n_q_heads, const int32_t* ctx_len,
                    int max_ctx, float scale, void* out, void* workspace, void* stream) {
@@ -399,8 +398,8 @@ int launch_decode8(const View8& v, const void* q, int dtype, int batch, int n_q_
 }
 
 // A chunk of query tokens, up to eight rows (tokens x heads) a block: float32 queries, whose products take two terms.
-size_t chunk8_workspace_bytes(int batch, int n_tok, int g, int n_kv_heads, int max_ctx) {
-  return workspace8_bytes((long long)batch * ((n_tok + A8_ROWS / g - 1) / (A8_ROWS / g)), n_kv_heads, max_ctx);
+size_t chunk8_workspace_bytes(int batch, int n_tok, int g, int n_kv_heads) {
+  return workspace8_bytes((long long)batch * ((n_tok + A8_ROWS / g - 1) / (A8_ROWS / g)), n_kv_heads);
 }
 int launch_chunk8(const View8& v, const void* q, int dtype, int batch, int n_tok, int n_q_heads, const int32_t* start,
                   const int32_t* n_valid, int max_ctx, float scale, void* out, void* workspace, void* stream) {
@@ -414,7 +413,7 @@ int launch_chunk8(const View8& v, const void* q, int dtype, int batch, int n_tok
   a.start = start;
   a.n_valid = n_valid;
   // (this workspace comes as it is)
-  const cudaError_t e = cudaMemsetAsync(workspace, 0, counter8_bytes((long long)batch * a.n_blk, v.n_kv_heads), (cudaStream_t)stream);
+  const cudaError_t e = cudaMemsetAsync((uint8_t*)workspace + part8_bytes(), 0, counter8_bytes((long long)batch * a.n_blk, v.n_kv_heads), (cudaStream_t)stream);
   if (e != cudaSuccess) return (int)e;
   return launch8(a, n_q_heads, scale, q, dtype, out, workspace, stream);
 }

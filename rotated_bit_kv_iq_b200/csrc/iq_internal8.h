@@ -25,10 +25,10 @@ struct View8 {
 
 int launch_append8(const View8& v, const void* k, const void* vsrc, int dtype, long long ks, long long vs, int batch, int n_new,
                    const int32_t* start, const int32_t* n_valid, void* stream);
-size_t decode8_workspace_bytes(int batch, int n_kv_heads, int max_ctx);
+size_t decode8_workspace_bytes(int batch, int n_kv_heads);
 int launch_decode8(const View8& v, const void* q, int dtype, int batch, int n_q_heads, const int32_t* ctx_len,
                    int max_ctx, float scale, void* out, void* workspace, void* stream);
-size_t chunk8_workspace_bytes(int batch, int n_tok, int g, int n_kv_heads, int max_ctx);
+size_t chunk8_workspace_bytes(int batch, int n_tok, int g, int n_kv_heads);
 int launch_chunk8(const View8& v, const void* q, int dtype, int batch, int n_tok, int n_q_heads, const int32_t* start,
                   const int32_t* n_valid, int max_ctx, float scale, void* out, void* workspace, void* stream);
 size_t prefill8_workspace_bytes(int batch, int n_tok, int n_q_heads, int n_kv_heads, int max_ctx);

@@ -7,7 +7,7 @@ namespace iq {
 
 size_t prefill8_workspace_bytes(int batch, int n_tok, int n_q_heads, int n_kv_heads, int max_ctx) {
   const int g = std::min(8, n_q_heads / n_kv_heads);
-  return std::max(pt_plan(batch, n_tok, g, n_kv_heads, max_ctx).bytes, chunk8_workspace_bytes(batch, n_tok, g, n_kv_heads, max_ctx));
+  return std::max(pt_plan(batch, n_tok, g, n_kv_heads, max_ctx).bytes, chunk8_workspace_bytes(batch, n_tok, g, n_kv_heads));
 }
 
 // 16-bit queries on tcgen05; float32 queries, whose outputs are to be right to 2^-20 or so, with two binary16 terms of q

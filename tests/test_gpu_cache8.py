@@ -278,6 +278,34 @@ def test_decode_with_many_tiles_a_cta(code):
             _check_rows(o[b], q[b].double().numpy(), *kv, 128 ** -0.5, dtype)
 
 
+def test_decode_calls_of_several_sizes_share_a_workspace():
+    """One workspace, large enough for each: a long sequence of one head, cut over all CTAs, then many groups."""
+    n, batch, hkv, ps, per = 20000, 40, 8, 64, 16
+    one = B.PagedCache8(1, 1, 64, 320, block_table=torch.arange(320, dtype=torch.int32, device=DEV).view(1, -1))
+    many = B.PagedCache8(1, hkv, ps, batch * per,
+                         block_table=torch.arange(batch * per, dtype=torch.int32, device=DEV).view(batch, per))
+    B.iq_append8(one, 0, *(_tokens(s, (1, n, 1, 128)).to(DEV) for s in (50, 51)), _i32([0]))
+    B.iq_append8(many, 0, *(_tokens(s, (batch, ps * per, hkv, 128)).to(DEV) for s in (52, 53)), _i32([0] * batch))
+    q1 = torch.randn((1, 8, 128), generator=torch.Generator().manual_seed(2)).to(F16).to(DEV)
+    q2 = torch.randn((batch, 4 * hkv, 128), generator=torch.Generator().manual_seed(3)).to(F16).to(DEV)
+    l1, l2 = _i32([n]), _i32([ps * per - 7 * i for i in range(batch)])
+    size = max(B.iq_decode8_workspace_size(1, 8, 1, 20480), B.iq_decode8_workspace_size(batch, 4 * hkv, hkv, ps * per))
+    shared = torch.zeros(size, dtype=torch.uint8, device=DEV)
+
+    def run(ws):
+        a, b = torch.full_like(q1, float("nan")), torch.full_like(q2, float("nan"))
+        B.iq_decode8_attention(one, 0, q1, l1, 20480, a, ws)
+        B.iq_decode8_attention(many, 0, q2, l2, ps * per, b, ws if ws is shared else torch.zeros_like(ws))
+        return a, b
+
+    a, b = run(torch.zeros_like(shared))
+    for _ in range(3):
+        x, y = run(shared)
+        assert torch.equal(x, a) and torch.equal(y, b)
+    assert one.status.item() == 0 and many.status.item() == 0
+    assert not torch.isnan(a).any() and not torch.isnan(b).any()
+
+
 @pytest.mark.parametrize("lens", [[0, 0], [1, 0], [40, 700], [3, 260]])
 def test_lengths_far_below_the_bound(lens):
     """max_ctx sizes the grid; the lengths decide what there is to share out."""
