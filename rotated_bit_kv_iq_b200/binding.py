@@ -533,6 +533,8 @@ def iq_append8(cache, layer, k, v, start_pos, n_valid=None, stream=None):
     x = k if k is not None else v
     if x is None:
         _bad(fn, "k or v wanted")
+    if x.dim() != 4:
+        _bad(fn, "[batch][n_new][Hkv][128] tensors wanted")
     batch, n = x.shape[0], x.shape[1]
     _batch8(fn, cache, batch)
     if batch == 0 or n == 0:
@@ -545,7 +547,8 @@ def iq_append8(cache, layer, k, v, start_pos, n_valid=None, stream=None):
         stride = t.stride(1) if n > 1 else t.stride(0) if batch > 1 else 0
         if (t.dtype != x.dtype or t.get_device() != dev or t.shape != (batch, n, cache.n_kv_heads, HEAD_DIM)
                 or t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != HEAD_DIM)
-                or (batch > 1 and t.stride(0) != n * stride)):
+                or (batch > 1 and t.stride(0) != n * stride)
+                or (batch * n > 1 and stride < cache.n_kv_heads * HEAD_DIM)):  # (a broadcast tensor's 0)
             _bad(fn, f"[{batch}][{n}][{cache.n_kv_heads}][128] tensors of one type, with contiguous heads and equally "
                      f"distant tokens, on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
         strides.append(stride)
@@ -628,7 +631,8 @@ def _rope_side(fn, name, x, y, dtype, dev, n):
     heads = x.shape[1] if x.dim() == 3 else 0
     for t in (x, y):
         if (t.dtype != dtype or t.get_device() != dev or t.shape != (n, heads, HEAD_DIM) or t.stride(2) != 1
-                or (heads > 1 and t.stride(1) != HEAD_DIM)):
+                or (heads > 1 and t.stride(1) != HEAD_DIM)
+                or (n > 1 and t.stride(0) < heads * HEAD_DIM)):  # (a broadcast tensor's 0)
             _bad(fn, f"{name}: [{n}][heads][128] tensors of one type with contiguous heads on cuda:{dev} wanted, got "
                      f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
     if n < 2:
@@ -646,6 +650,8 @@ def iq_rope(q, k, positions, freq, q_out=None, k_out=None, layout="half", mscale
     x = q if q is not None else k
     if x is None:
         _bad(fn, "q or k wanted")
+    if x.dim() != 3:
+        _bad(fn, "[n_tokens][heads][128] tensors wanted")
     dev, n, pairs = x.get_device(), x.shape[0], freq.numel()
     if n == 0:
         return

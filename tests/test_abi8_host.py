@@ -196,3 +196,19 @@ def test_binding_refuses_tensors_of_another_device_shape_or_type(lib):
             B.iq_decode8_attention(c, 0, qq, s, 32, oo, w)
     with pytest.raises(ValueError):
         B.iq_append8(c, 0, k, None, s)  # nothing wrong but the device
+
+
+def test_binding_refuses_broadcast_rows(lib):
+    """Rows that share their memory have a stride of 0, which would be taken for the default."""
+    c = B.PagedCache8(1, 2, 32, 4, device="cpu")
+    for k in (torch.zeros(1, 1, 2, 128).expand(1, 3, 2, 128), torch.zeros(1, 1, 2, 128).expand(3, 1, 2, 128),
+              torch.zeros(1, 1, 2, 128).expand(2, 4, 2, 128), torch.zeros(3, 2, 128)):
+        with pytest.raises(ValueError, match="wanted") as e:
+            B.iq_append8(c, 0, k, None, torch.zeros(k.shape[0], dtype=torch.int32))
+        assert "CUDA tensors wanted" not in str(e.value)
+    x, y = torch.zeros(1, 2, 128).expand(4, 2, 128), torch.zeros(4, 2, 128)
+    pos, freq = torch.zeros(4, dtype=torch.int32), torch.zeros(64, dtype=torch.float64)
+    for q, o in ((x, y), (y, x), (x, None), (torch.zeros(128), None)):
+        with pytest.raises(ValueError, match="wanted") as e:
+            B.iq_rope(q, None, pos, freq, q_out=o)
+        assert "CUDA tensors wanted" not in str(e.value)
