@@ -39,24 +39,25 @@ __device__ __forceinline__ void flag(const iq_pages& p, uint32_t bit) {
   if (p.status_dev) atomicOr(p.status_dev, bit);
 }
 
-// Exclusive prefix sum over the block's threads; *total gets the sum.  scratch: PG_WARPS + 1 ints.
-__device__ __forceinline__ int block_scan(int x, int* scratch, int* total) {
+// Exclusive prefix sum over the block's threads; *total gets the sum.  scratch: PG_WARPS + 1 numbers.
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* scratch, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
+  T incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    const T y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   __syncthreads();
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int own = scratch[lane];
-    int s = own;
+    const T own = scratch[lane];
+    T s = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      const T y = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += y;
     }
     scratch[lane] = s - own;
@@ -102,10 +103,12 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(iq_pages p, co
   __shared__ int s_id[IQ_PAGES_MAX_LIST];
   __shared__ int s_need[IQ_PAGES_MAX_LIST];
   __shared__ int scratch[PG_WARPS + 1];
+  __shared__ long long wide[PG_WARPS + 1];
   const int tid = threadIdx.x;
   for (int i = tid; i < n; i += PG_THREADS) s_id[i] = ids[i];
   __syncthreads();
-  int need[PG_PER], sum = 0;
+  int need[PG_PER];
+  long long sum = 0;  // (what a long list asks for may pass 32 bits, however few pages there are)
 #pragma unroll
   for (int k = 0; k < PG_PER; ++k) {
     const int i = tid * PG_PER + k;
@@ -125,8 +128,8 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(iq_pages p, co
     }
     sum += max(0, need[k]);
   }
-  int total;
-  int at = block_scan(sum, scratch, &total);
+  long long total;
+  long long at = block_scan(sum, wide, &total);
   const int n_free = rank_pages(p.n_pages, scratch, [&](int g) { return p.ref_dev[g] <= 0; },
                                 [&](int rank, int g) { if (rank < total) w.remap[rank] = g; });
 #pragma unroll
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_extend_kernel(iq_pages p, co
     int start = -1;  // first free-page rank of this entry; -1: nothing to take
     if (need[k] >= 0) {
       if (at + need[k] > n_free) flag(p, IQ_DEVERR_NOPAGE);
-      else start = at;
+      else start = (int)at;
       at += need[k];
     }
     s_need[i] = start;

@@ -118,6 +118,18 @@ def test_running_out_of_pages():
     t.check()
 
 
+def test_requests_whose_sum_passes_32_bits():
+    """2048 sequences of up to 2^20 pages each ask for 2^31 of a pool's 8: all but the first few are refused."""
+    n, per = 2050, 1 << 20
+    t = B.PageTable(n, per, 32, 8)
+    lens = [33] + [per * 32] * (n - 2) + [1]
+    B.iq_pages_extend(t, _i32(list(range(n))), _i32(lens))
+    assert t.status.item() == B.IQ_DEVERR_NOPAGE
+    assert t.seq_len.tolist() == [33] + [0] * (n - 1)
+    assert t.ref.tolist() == [1, 1] + [0] * 6
+    assert t.block_table[0, :3].tolist() == [0, 1, -1] and int((t.block_table >= 0).sum()) == 2
+
+
 def test_forks_of_forks_share_pages_and_a_whole_page_needs_none():
     t = Both(8, 3, 32, 16)
     t.extend([0, 1], [64, 65])
