@@ -86,6 +86,7 @@ size_t iq_decode8_workspace_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_
  *   q_dev, out_dev : [batch][n_q_heads][128] of `dtype` (IQ_F16, IQ_BF16, IQ_F32); sums in float32.
  *   scale          : finite and > 0 (1/sqrt(128) for plain attention).
  * ctx_len, max_ctx, workspace, batch <= 2048 and the group size of 1..8 as for iq_decode_attention:
+ * max_ctx at most 2^30, and 2^35 / Hkv (IQ_ERR_UNSUPPORTED above);
  * ctx_len 0 gives a zero row, values outside [0, max_ctx] are clamped and flagged (IQ_DEVERR_CTX).
  * Tokens of a page outside the pool are left out and flagged (IQ_DEVERR_PAGE). */
 iq_status iq_decode8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,
@@ -102,7 +103,8 @@ size_t iq_prefill8_workspace_size(int32_t batch, int32_t n_tokens, int32_t n_q_h
  *   n_valid_dev    : int32 [batch] or NULL: only the first n_valid[b] tokens (clamped to 0..n_tokens,
  *                    flagged) are there; the rows of `out` behind them are left as they were.
  *   start_pos      : values outside [0, max_ctx - n_valid[b]] are clamped and flagged.
- * Other arguments as for iq_decode8_attention. */
+ * Other arguments as for iq_decode8_attention.  At most 2^27 kv heads' tokens (batch Hkv n_tokens), and 2^31
+ * steps of 128 keys by the blocks of 256 / G tokens (IQ_ERR_UNSUPPORTED above). */
 iq_status iq_prefill8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,
                                 int32_t n_tokens, int32_t n_q_heads, const int32_t* start_pos_dev,
                                 const int32_t* n_valid_dev, int32_t max_ctx, float scale, void* out_dev,

@@ -43,6 +43,17 @@ static int64_t capacity8(const iq_cache8* c) {
   return (int64_t)c->page_size * (c->block_table_dev ? c->max_pages_per_seq : 1);
 }
 
+// The kernels count tiles of a sequence's heads, and steps of a prefill call, in 32 bits.
+static bool context_ok(const iq_cache8* c, int32_t max_ctx) {
+  return max_ctx <= 1 << 30 && (int64_t)max_ctx * c->n_kv_heads <= (int64_t)1 << 35;
+}
+static bool prefill_ok(const iq_cache8* c, int32_t batch, int32_t n_tokens, int32_t n_q_heads, int32_t max_ctx) {
+  const int64_t rows = (int64_t)batch * c->n_kv_heads * n_tokens;
+  if (rows > (int64_t)1 << 27 || !context_ok(c, max_ctx)) return false;
+  const int32_t tq = 256 / (n_q_heads / c->n_kv_heads);
+  return (int64_t)batch * c->n_kv_heads * ((n_tokens + tq - 1) / tq) * ((int64_t)max_ctx / 128 + 1) < (int64_t)1 << 31;
+}
+
 static iq_status check_heads(const iq_cache8* c, int32_t n_q_heads) {
   if (n_q_heads < 1 || n_q_heads % c->n_kv_heads != 0) return IQ_ERR_INVALID_ARG;
   return n_q_heads / c->n_kv_heads > 8 ? IQ_ERR_UNSUPPORTED : IQ_OK;
@@ -142,6 +153,7 @@ iq_status iq_decode8_attention(const iq_cache8* cache, int32_t layer, const void
   IQ_TRY(check_heads(cache, n_q_heads));
   if (!cache->block_table_dev && batch > cache->n_pages) return IQ_ERR_CAPACITY;
   if ((int64_t)max_ctx > capacity8(cache)) return IQ_ERR_CAPACITY;
+  if (!context_ok(cache, max_ctx)) return IQ_ERR_UNSUPPORTED;
   if (!aligned_to(q_dev, 16) || !aligned_to(out_dev, 16) || !aligned_to(ctx_len_dev, 4)) return IQ_ERR_ALIGNMENT;
   IQ_TRY(check_ws(workspace_dev, workspace_bytes, decode8_workspace_bytes(batch, cache->n_kv_heads)));
   return result(launch_decode8(view8(cache, layer), q_dev, dtype, batch, n_q_heads, ctx_len_dev, max_ctx, scale, out_dev,
@@ -165,7 +177,7 @@ iq_status iq_prefill8_attention(const iq_cache8* cache, int32_t layer, const voi
   IQ_TRY(check_heads(cache, n_q_heads));
   if (!cache->block_table_dev && batch > cache->n_pages) return IQ_ERR_CAPACITY;
   if ((int64_t)max_ctx > capacity8(cache)) return IQ_ERR_CAPACITY;
-  if ((int64_t)batch * cache->n_kv_heads * n_tokens > (int64_t)1 << 27) return IQ_ERR_UNSUPPORTED;
+  if (!prefill_ok(cache, batch, n_tokens, n_q_heads, max_ctx)) return IQ_ERR_UNSUPPORTED;
   if (!aligned_to(q_dev, 16) || !aligned_to(out_dev, 16) || !aligned_to(start_pos_dev, 4) || !aligned_to(n_valid_dev, 4))
     return IQ_ERR_ALIGNMENT;
   IQ_TRY(check_ws(workspace_dev, workspace_bytes,

@@ -230,7 +230,7 @@ int launch_append8(const View8& v, const void* k, const void* vsrc, int dtype, l
   a.vs = vs;
   a.batch = batch;
   a.n_new = n_new;
-  a.tiles = (n_new + 2 * TILE_TOKENS - 2) / TILE_TOKENS;
+  a.tiles = (int)(((long long)n_new + 2 * TILE_TOKENS - 2) / TILE_TOKENS);
   a.start = start;
   a.n_valid = n_valid;
   const long long units = (long long)batch * a.tiles * 2 * v.n_kv_heads;
@@ -251,9 +251,9 @@ int launch_append8(const View8& v, const void* k, const void* vsrc, int dtype, l
 
 // One thread per (kv head, token, 16-byte chunk): code * scale.
 __global__ void export8_kernel(View8 v, int kv, int seq, int t0, int n, float* values) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  const int tok = i >> 3, c = i & 7, head = blockIdx.y;
-  if (tok >= n) return;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int tok = (int)(i >> 3), c = (int)(i & 7), head = blockIdx.y;
+  if (i >= 8ll * n) return;
   uint32_t err = 0;
   const long long pos = (long long)t0 + tok;
   const int page = find_page8(v, seq, pos, &err);

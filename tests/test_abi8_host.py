@@ -93,6 +93,13 @@ def test_attention8_rejects_bad_arguments(lib):
             assert f(_cache(), **kw) == want, (f.__name__, kw)
     assert dec(_cache(block_table_dev=0xB0000, max_pages_per_seq=1), batch=2049) == B.IQ_ERR_UNSUPPORTED
     assert dec(_cache(), max_ctx=-1) == B.IQ_ERR_INVALID_ARG
+    # lengths that tiles or steps of 32 bits could not count
+    far = dict(block_table_dev=0xB0000, page_size=1 << 20, max_pages_per_seq=2047)
+    assert dec(_cache(**far), max_ctx=(1 << 30) + 1) == B.IQ_ERR_UNSUPPORTED
+    assert dec(_cache(n_kv_heads=64, **far), hq=64, max_ctx=(1 << 29) + 1) == B.IQ_ERR_UNSUPPORTED
+    assert pre(_cache(**far), max_ctx=(1 << 30) + 1) == B.IQ_ERR_UNSUPPORTED
+    assert pre(_cache(**far), batch=64, n=64 * 64, max_ctx=1 << 28) == B.IQ_ERR_UNSUPPORTED
+    assert pre(_cache(**far), batch=64, n=(1 << 20) + 1, max_ctx=1 << 21) == B.IQ_ERR_UNSUPPORTED
     assert pre(_cache(), n=33) == B.IQ_ERR_INVALID_ARG  # max_ctx below the chunk
     assert pre(_cache(), valid=0x70002) == B.IQ_ERR_ALIGNMENT
     assert B.iq_decode8_workspace_size(1, 8, 0, 10) == 0 and B.iq_prefill8_workspace_size(1, 1, 1, 2, 10) == 0
