@@ -18,6 +18,7 @@ namespace iq {
 constexpr int D8_WARPS = 12;
 constexpr int D8_THREADS = 32 * D8_WARPS;
 constexpr int D8_NB = 2;                                       // tile records in a warp's ring
+constexpr int D8_UNCUT = 2 * D8_WARPS;                         // tiles of a group that is not cut
 constexpr int D8_SMEM = D8_WARPS * D8_NB * TILE8_BYTES;        // (at a segment's end: the warps' value sums)
 static_assert(D8_WARPS * A8_ROWS * D * 4 <= D8_SMEM, "value sums in the rings' place");
 
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __syncthreads();
   // Short groups, of two rounds of the warps at the most, are not cut: CTA c takes groups c, c + grid, ... whole, and there
   // is nothing to merge (a 512-token layer of two kv heads: 9 us a call, 15 cut).
-  const bool uncut = most <= 2 * D8_WARPS;
+  const bool uncut = most <= D8_UNCUT;
   if (!uncut && lo >= hi) return;
   int e = 0, kvh = 0, nt = 0, tile0 = 0;
   D8Entry x = {};
@@ -412,9 +413,11 @@ int launch_chunk8(const View8& v, const void* q, int dtype, int batch, int n_tok
   a.n_blk = (n_tok + a.tq - 1) / a.tq;
   a.start = start;
   a.n_valid = n_valid;
-  // (this workspace comes as it is)
-  const cudaError_t e = cudaMemsetAsync((uint8_t*)workspace + part8_bytes(), 0, counter8_bytes((long long)batch * a.n_blk, v.n_kv_heads), (cudaStream_t)stream);
-  if (e != cudaSuccess) return (int)e;
+  if (max_ctx > D8_UNCUT * TILE_TOKENS) {  // groups may be cut, and this workspace comes as it is
+    const cudaError_t e = cudaMemsetAsync((uint8_t*)workspace + part8_bytes(), 0,
+                                          counter8_bytes((long long)batch * a.n_blk, v.n_kv_heads), (cudaStream_t)stream);
+    if (e != cudaSuccess) return (int)e;
+  }
   return launch8(a, n_q_heads, scale, q, dtype, out, workspace, stream);
 }
 
