@@ -19,11 +19,9 @@
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
 // issues the MMAs, 17 finds the records and their scales.
 //
-// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 296 us, 813 TFLOP/s, 49% of cuBLAS's bf16 rate.  Per
-// step of 5,200 cycles a CTA's MMAs take 2,500 (the 64-key score products reach 63% of the MMA rate, being fed from shared
-// memory on both sides; the P V products all of it); the softmax warps, alone on their schedulers, 2,900, bound by the
-// exponentials (MUFU); with the expansion's two warps beside them on each scheduler (14% of the time) and the hand-overs
-// the two overlap to less than half.
+// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 296-311 us, 773-813 TFLOP/s, 46-49% of cuBLAS's bf16
+// rate.  Of a step's 5,200 cycles the MMAs take 2,500 (a 64-key score product runs at 64% of the MMA rate: 50 cycles for
+// 32) and the softmax, on its own, 2,900, bound by the exponentials (MUFU); the two overlap to less than half.
 #pragma once
 #include <algorithm>
 
