@@ -4,6 +4,8 @@
 // rotary_dim / 2 sines and cosines once for all heads (the angle in turns, reduced to [-1/2, 1/2] in
 // double; sine and cosine of that fraction in float32), then turn what they loaded.  A thread owns whole
 // pairs, so that a call may work in place.  Bound by memory: every value read once and written once.
+// 8192 tokens of 40 heads in 16 bits: 29 us, 91% of the copy rate (48 with the angles before the loads); 16 tokens: 5.6 us,
+// latency.
 #include <algorithm>
 
 #include "iq_cache8.cuh"
