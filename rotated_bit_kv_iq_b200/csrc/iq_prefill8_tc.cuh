@@ -58,11 +58,11 @@ struct PtSmem {
 };
 static_assert(PtSmem::bytes <= 232448, "one CTA's shared memory");
 
-// mbarriers: K and V of step parity expanded / free again; by half-step parity: both tiles' scores ready; by tile and
-// half-step parity (2 t + b): P written; the last O += P V done, the one before it; queries; records of step n mod 4
+// mbarriers: K and V of step parity expanded / free again; by tile and half-step parity (2 t + b): scores ready, P
+// written; the last O += P V done, the one before it; queries; records of step n mod 4
 // located / taken.
-enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 10, TB_ODONE = 14, TB_OLAST = 15,
-       TB_Q = 16, TB_DRAIN = 17, TB_LFULL = 18, TB_LFREE = 22, TB_COUNT = 26 };
+enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 12, TB_ODONE = 16, TB_OLAST = 17,
+       TB_Q = 18, TB_DRAIN = 19, TB_LFULL = 20, TB_LFREE = 24, TB_COUNT = 28 };
 
 struct PtArgs {
   View8 v;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         const int halves = 2 * (s.k1 - s.k0);
         for (int i = 0; i < halves; ++i, ++done) {
           const int buf = done & 1;
-          ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + buf], (done >> 1) & 1, abort, a.v.status));
+          ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + 2 * t + buf], (done >> 1) & 1, abort, a.v.status));
           if (!ok) break;
           tc_fence_after();
           const int slot = 2 * ((n + (i >> 1)) & 7) + (i & 1);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               // O += P V of the half-step before is done: the scores of the next one, or at the end a barrier of its
               // own, are signalled after it
               const bool next = i + 1 < halves;
-              ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
+              ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + 2 * t + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
                                                 : pt_wait(&bars[TB_ODONE], seg & 1, abort, a.v.status));
               if (!ok) break;
               tc_fence_after();
@@ -396,7 +396,6 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       } else {  // no row of this tile: not ahead of the tile that has rows
         ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_OLAST], seg & 1, abort, a.v.status));
         if (!ok) break;
-        done += 2 * (s.k1 - s.k0);
       }
       n += s.k1 - s.k0;
       ++seg;
@@ -549,12 +548,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         wait(TB_KFULL + (n & 1), n >> 1);
         tc_fence_after();
         if (elect_one()) {
-          scores(0, n, 0);
-          if (tiles == 2) scores(1, n, 0);
-          umma_commit(&bars[TB_SFULL]);
-          scores(0, n, 1);
-          if (tiles == 2) scores(1, n, 1);
-          umma_commit(&bars[TB_SFULL + 1]);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (t < tiles) {
+                scores(t, n, b);
+                umma_commit(&bars[TB_SFULL + 2 * t + b]);
+              }
           umma_commit(&bars[TB_KFREE + (n & 1)]);
         }
         __syncwarp();
@@ -573,14 +574,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
                 tc_fence_after();
                 if (elect_one()) {
                   umma_f16_ts_k64(tm + PT_O_COL + 128 * t, tm + PT_S_COL + 128 * t + 64 * b, dv + 2048 * (n & 1) + 512 * b, idO, i + b > 0);
-                  if (!last) scores(t, n + 1, b);
+                  if (!last) {
+                    scores(t, n + 1, b);
+                    umma_commit(&bars[TB_SFULL + 2 * t + b]);
+                  }
                 }
                 __syncwarp();
               }
             }
             if (elect_one()) {
-              if (!last) umma_commit(&bars[TB_SFULL + b]);
-              else umma_commit(&bars[b ? TB_OLAST : TB_ODONE]);
+              if (last) umma_commit(&bars[b ? TB_OLAST : TB_ODONE]);
               if (b) {
                 umma_commit(&bars[TB_VFREE + (n & 1)]);
                 if (!last) umma_commit(&bars[TB_KFREE + ((n + 1) & 1)]);
