@@ -17,7 +17,7 @@
 // causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block cut by a run's
 // end leaves partials, which a second kernel merges in order.
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
-// issues the MMAs, 17 finds the records and their scales.
+// and 18 issue the two tiles' MMAs, 17 finds the records and their scales.
 //
 // Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 296-311 us, 773-813 TFLOP/s, 46-49% of cuBLAS's bf16
 // rate.  Of a step's 5,200 cycles the MMAs take 2,500 (a 64-key score product runs at 64% of the MMA rate: 50 cycles for
@@ -59,10 +59,10 @@ struct PtSmem {
 static_assert(PtSmem::bytes <= 232448, "one CTA's shared memory");
 
 // mbarriers: K and V of step parity expanded / free again; by tile and half-step parity (2 t + b): scores ready, P
-// written; the last O += P V done, the one before it; queries; records of step n mod 4
+// written; by tile: a segment's last O += P V done, the one before it; queries; all MMAs done; records of step n mod 4
 // located / taken.
-enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 12, TB_ODONE = 16, TB_OLAST = 17,
-       TB_Q = 18, TB_DRAIN = 19, TB_LFULL = 20, TB_LFREE = 24, TB_COUNT = 28 };
+enum { TB_KFULL = 0, TB_KFREE = 2, TB_VFULL = 4, TB_VFREE = 6, TB_SFULL = 8, TB_PFULL = 12, TB_ODONE = 16, TB_OLAST = 18,
+       TB_Q = 20, TB_DRAIN = 21, TB_LFULL = 22, TB_LFREE = 26, TB_COUNT = 30 };
 
 struct PtArgs {
   View8 v;
@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       // one arrival a warp (of all 32 lanes' it would be 32 in a row)
       const bool expanded = i == TB_KFULL || i == TB_KFULL + 1 || i == TB_VFULL || i == TB_VFULL + 1;
       const bool written = i >= TB_PFULL && i < TB_PFULL + 4;
-      const int count = expanded || written ? 4 : i >= TB_LFREE || i == TB_Q ? 8 : 1;
+      const bool freed = i == TB_KFREE || i == TB_KFREE + 1 || i == TB_VFREE || i == TB_VFREE + 1 || i == TB_DRAIN;  // by both tiles
+      const int count = expanded || written ? 4 : i >= TB_LFREE || i == TB_Q ? 8 : freed ? 2 : 1;
       mbar_init(&bars[i], count);
     }
     mbar_fence_init();
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               // own, are signalled after it
               const bool next = i + 1 < halves;
               ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + 2 * t + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
-                                                : pt_wait(&bars[TB_ODONE], seg & 1, abort, a.v.status));
+                                                : pt_wait(&bars[TB_ODONE + t], seg & 1, abort, a.v.status));
               if (!ok) break;
               tc_fence_after();
               l *= al;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[TB_PFULL + 2 * t + buf]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_OLAST], seg & 1, abort, a.v.status));
+        if (ok) ok = __all_sync(0xffffffffu, pt_wait(&bars[TB_OLAST + t], seg & 1, abort, a.v.status));
         if (!ok) break;
         tc_fence_after();
         const bool whole = s.k0 == 0 && s.k1 == s.x.steps;
@@ -393,8 +394,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         }
         __syncwarp();
         tc_fence_before();
-      } else {  // no row of this tile: not ahead of the tile that has rows
-        ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_OLAST], seg & 1, abort, a.v.status));
+      } else {  // no row of this tile: no more than a segment ahead of the tile that has rows
+        ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_OLAST + t], seg & 1, abort, a.v.status));
         if (!ok) break;
       }
       n += s.k1 - s.k0;
@@ -517,29 +518,34 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           }
         }
       }
-    } else if (warp == 16) {
-      // ==== MMAs.  The tensor core takes its operands' descriptors from uniform registers: the warp runs as one, on
+    } else if (warp == 16 || warp == 18) {
+      // ==== MMAs of tile t, a warp for each: what one waits for does not hold up the other, whose MMAs the tensor core
+      // has meanwhile.  The tensor core takes its operands' descriptors from uniform registers: a warp runs as one, on
       // counts that are broadcast and in loops without an early end (where a wait has given up the others do too, soon,
       // and what is computed then is nobody's), so that the compiler keeps them there.  With descriptors from one
       // lane's registers an MMA took about 94 cycles to issue, not 52.
       const uint32_t idS = umma_idesc_f16(128, 64), idO = umma_idesc_f16(128, 128) | UMMA_B_MN_MAJOR;
+      const int t = __shfl_sync(0xffffffffu, (int)(warp == 18), 0);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm = __shfl_sync(0xffffffffu, smem_addr(smem), 0);
-      const uint64_t dq = umma_sdesc_sw128(sm + SM::q), dk = umma_sdesc_sw128(sm + SM::k), dv = umma_sdesc_sw128_mn(sm + SM::v, 128);
-      uint32_t n = 0, seg = 0, written[2] = {0, 0};  // steps, segments; half-steps of P by tile
+      const uint32_t tS = tm + PT_S_COL + 128 * t, tO = tm + PT_O_COL + 128 * t;
+      const uint64_t dq = umma_sdesc_sw128(sm + SM::q + 32768 * t), dk = umma_sdesc_sw128(sm + SM::k),
+                     dv = umma_sdesc_sw128_mn(sm + SM::v, 128);
+      uint32_t n = 0, seg = 0, written = 0;  // steps, segments; half-steps of P
       auto wait = [&](int bar, uint32_t parity) {
         pt_wait(&bars[bar], parity & 1, abort, a.v.status);
         __syncwarp();
       };
-      // scores of tile t's half-step h of step m: 64 keys, 8192 bytes of a buffer's blocks (512 descriptor units); tiles
-      // and buffers are 32 KB (2048) apart
-      auto scores = [&](int t, uint32_t m, int h) {
-        umma_f16_k128(tm + PT_S_COL + 128 * t + 64 * h, dq + 2048 * t, dk + 2048 * (m & 1) + 512 * h, idS);
+      // scores of half-step h of step m: 64 keys, 8192 bytes of a buffer's blocks (512 descriptor units); buffers are 32 KB
+      // (2048) apart
+      auto scores = [&](uint32_t m, int h) {
+        umma_f16_k128(tS + 64 * h, dq, dk + 2048 * (m & 1) + 512 * h, idS);
+        umma_commit(&bars[TB_SFULL + 2 * t + h]);
       };
       bool more = true;
       do {
-        const int tiles = __shfl_sync(0xffffffffu, s.x.n_live * G > PT_TILE ? 2 : 1, 0);
+        const bool rows = __shfl_sync(0xffffffffu, (int)(s.x.n_live * G > PT_TILE * t), 0);  // of this tile, in the block
         const int steps = __shfl_sync(0xffffffffu, s.k1 - s.k0, 0);
-        if (lane == 0) {  // where the block is cut, for the merge
+        if (t == 0 && lane == 0) {  // where the block is cut, for the merge
           int2* const cut = a.cut + (size_t)s.e * Hkv + s.kvh;
           if (s.k0 == 0) cut->x = 2 * c + (s.pos == 0 ? 0 : 1);
           if (s.k1 == s.x.steps) cut->y = c;
@@ -548,14 +554,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         wait(TB_KFULL + (n & 1), n >> 1);
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (t < tiles) {
-                scores(t, n, b);
-                umma_commit(&bars[TB_SFULL + 2 * t + b]);
-              }
+          if (rows) {
+            scores(n, 0);
+            scores(n, 1);
+          }
           umma_commit(&bars[TB_KFREE + (n & 1)]);
         }
         __syncwarp();
@@ -566,24 +568,17 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           if (!last) wait(TB_KFULL + ((n + 1) & 1), (n + 1) >> 1);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (t < tiles) {
-                wait(TB_PFULL + 2 * t + b, written[t] >> 1);
-                ++written[t];
-                tc_fence_after();
-                if (elect_one()) {
-                  umma_f16_ts_k64(tm + PT_O_COL + 128 * t, tm + PT_S_COL + 128 * t + 64 * b, dv + 2048 * (n & 1) + 512 * b, idO, i + b > 0);
-                  if (!last) {
-                    scores(t, n + 1, b);
-                    umma_commit(&bars[TB_SFULL + 2 * t + b]);
-                  }
-                }
-                __syncwarp();
-              }
+            if (rows) {
+              wait(TB_PFULL + 2 * t + b, written >> 1);
+              ++written;
+              tc_fence_after();
             }
             if (elect_one()) {
-              if (last) umma_commit(&bars[b ? TB_OLAST : TB_ODONE]);
+              if (rows) {
+                umma_f16_ts_k64(tO, tS + 64 * b, dv + 2048 * (n & 1) + 512 * b, idO, i + b > 0);
+                if (!last) scores(n + 1, b);
+              }
+              if (last) umma_commit(&bars[(b ? TB_OLAST : TB_ODONE) + t]);
               if (b) {
                 umma_commit(&bars[TB_VFREE + (n & 1)]);
                 if (!last) umma_commit(&bars[TB_KFREE + ((n + 1) & 1)]);
