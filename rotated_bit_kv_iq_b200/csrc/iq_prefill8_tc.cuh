@@ -9,9 +9,10 @@
 // Each tile has two S buffers: while the softmax is at one half-step's scores the tensor core adds the P of the half-step
 // before and makes the scores of the one after.  (One buffer of 128 keys a tile: 318 us on the 2048-token chunk.)
 // The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and the V
-// scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is a running maximum of
-// s + log2 v that follows only once it has been passed by 2^8: O is then rescaled in tensor memory, rarely.  p' is one
-// binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are float32.
+// scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is the first half-step's maximum
+// of s + log2 v, and follows only once the p' of a half-step add up to more than 2^15: O is then rescaled in tensor memory,
+// rarely.  p' is one binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are
+// float32.
 //
 // Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that neither
 // causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block cut by a run's
@@ -39,7 +40,7 @@ constexpr int PT_THREADS = 640;
 constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
-constexpr float PT_SLACK = 8.f;
+constexpr float PT_TOP = 32768.f;  // 2^15: the most that p' of a half-step add up to (binary16 reaches 2^16)
 
 struct PtSmem {
   static constexpr int q = 0;                 // [tile] 128 rows x 128 coordinates
@@ -283,39 +284,30 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           const float2 ws = reinterpret_cast<const float2*>(smem + SM::w)[slot];
           // some key is not seen by some row of the warp, or some record is not there
           const bool some = __any_sync(0xffffffffu, lim < 63) || !(lvs.x == lvs.x) || !(lvs.y == lvs.y);
-          // One pass: the scores of a record, their maximum, and p' under the ref that stands.  P waits in registers
-          // until the maximum of the half-step is known; where it has passed ref by more than the slack (a block's
-          // first half-step, and rarely after it) the pass is made again under the new ref.
+          auto record = [&](int b, uint32_t (&x)[32]) {  // scores of record b; keys that the row does not see: -inf
+            tmem_ld32(tS + 64 * buf + 32 * b, x);
+            tmem_wait_ld(x);
+            if (some) {
+              const float lv = b ? lvs.y : lvs.x;
+              const int last = lv == lv ? lim - 32 * b : -1;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = k <= last ? x[k] : 0xFF800000u;
+            }
+          };
+          // p' of the half-step under the ref that stands; P waits in registers.  The row's sum, which is
+          // needed anyway, tells whether a p' has become too large: no maximum has to be found.
           uint32_t pp[32];
-          float add_l;
+          float add_l, top;
           auto pass = [&](float at) {
-            float mo = -CUDART_INF_F;
-            add_l = 0.f;
+            add_l = top = 0.f;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               uint32_t x[32];
-              tmem_ld32(tS + 64 * buf + 32 * b, x);
+              record(b, x);
               const float lv = b ? lvs.y : lvs.x;
               const bool here = lv == lv;
               const float f1 = here ? (b ? ks.y : ks.x) * qs : 1.f, add1 = here ? lv - at : 0.f;
               const uint64_t ff = f2(f1, f1), add = f2(add1, add1);
-              tmem_wait_ld(x);
-              if (some) {
-                const int last = here ? lim - 32 * b : -1;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[k] = k <= last ? x[k] : 0xFF800000u;
-              }
-              float mx[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mx[k] = __uint_as_float(x[k]);
-#pragma unroll
-              for (int k = 4; k < 28; k += 8)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], fmaxf(__uint_as_float(x[k + j]), __uint_as_float(x[k + j + 4])));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(x[28 + j]));
-              const float m1 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              if (m1 > -CUDART_INF_F) mo = fmaxf(mo, fmaf(m1, f1, here ? lv : 0.f));
               uint64_t sum[2] = {0, 0};
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
@@ -328,36 +320,54 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               }
               float s0, s1;
               f2s(add2(sum[0], sum[1]), s0, s1);
+              top += s0 + s1;
               add_l = fmaf(s0 + s1, b ? ws.y : ws.x, add_l);
             }
-            return mo;
           };
-          const float mo = pass(ref == -CUDART_INF_F ? 0.f : ref);
-          const bool up = i == 0 || mo > ref + PT_SLACK;
-          if (__any_sync(0xffffffffu, up)) {
-            const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
-            if (up) ref = mo;
-            if (i > 0) {
-              // O += P V of the half-step before is done: the scores of the next one, or at the end a barrier of its
-              // own, are signalled after it
-              const bool next = i + 1 < halves;
-              ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + 2 * t + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
-                                                : pt_wait(&bars[TB_ODONE + t], seg & 1, abort, a.v.status));
-              if (!ok) break;
-              tc_fence_after();
-              l *= al;
+          // A block's first half-step, and rarely one after it: ref becomes the half-step's maximum first
+          bool up = i == 0;
+          for (bool first = true;; first = false) {
+            if (__any_sync(0xffffffffu, up)) {
+              float mo = -CUDART_INF_F;
 #pragma unroll 1
-              for (int b = 0; b < 8; ++b) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * b, o);
-                tmem_wait_ld(o);
+              for (int b = 0; b < 2; ++b) {
+                uint32_t x[32];
+                record(b, x);
+                float m1 = -CUDART_INF_F;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                tmem_st16(tO + 16 * b, o);
+                for (int k = 0; k < 32; k += 2) m1 = fmaxf(m1, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+                const float lv = b ? lvs.y : lvs.x;
+                if (m1 > -CUDART_INF_F) mo = fmaxf(mo, lv == lv ? fmaf(m1, (b ? ks.y : ks.x) * qs, lv) : m1);
               }
+              const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
+              if (up) ref = mo;
+              if (i > 0) {
+                // O += P V of the half-step before is done: the scores of the next one, or at the end a barrier of its
+                // own, are signalled after it
+                const bool next = i + 1 < halves;
+                ok = __all_sync(0xffffffffu, next ? pt_wait(&bars[TB_SFULL + 2 * t + (buf ^ 1)], ((done + 1) >> 1) & 1, abort, a.v.status)
+                                                  : pt_wait(&bars[TB_ODONE + t], seg & 1, abort, a.v.status));
+                if (!ok) break;
+                tc_fence_after();
+                l *= al;
+#pragma unroll 1
+                for (int b = 0; b < 8; ++b) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + 16 * b, o);
+                  tmem_wait_ld(o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                  tmem_st16(tO + 16 * b, o);
+                }
+              }
+              first = false;
             }
             pass(ref == -CUDART_INF_F ? 0.f : ref);
+            if (!first) break;
+            up = !(top <= PT_TOP) || (ref == -CUDART_INF_F && lim >= 0);
+            if (!__any_sync(0xffffffffu, up)) break;
           }
+          if (!ok) break;
           l += add_l;
           // P over the columns of S
 #pragma unroll
