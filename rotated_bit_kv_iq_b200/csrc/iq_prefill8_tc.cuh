@@ -277,6 +277,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           ok = __all_sync(0xffffffffu, ok && pt_wait(&bars[TB_SFULL + 2 * t + buf], (done >> 1) & 1, abort, a.v.status));
           if (!ok) break;
           tc_fence_after();
+          uint32_t x[32];
+          tmem_ld32(tS + 64 * buf, x);  // under way while the scales are looked up
           const int slot = 2 * ((n + (i >> 1)) & 7) + (i & 1);
           const int lim = qpos - PT_BN * s.k0 - 64 * i;  // keys 0 .. lim of the half-step
           const float2 ks = reinterpret_cast<const float2*>(smem + SM::ks)[slot];
@@ -284,8 +286,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           const float2 ws = reinterpret_cast<const float2*>(smem + SM::w)[slot];
           // some key is not seen by some row of the warp, or some record is not there
           const bool some = __any_sync(0xffffffffu, lim < 63) || !(lvs.x == lvs.x) || !(lvs.y == lvs.y);
-          auto record = [&](int b, uint32_t (&x)[32]) {  // scores of record b; keys that the row does not see: -inf
-            tmem_ld32(tS + 64 * buf + 32 * b, x);
+          auto record = [&](int b) {  // scores of record b, whose load was started; keys that the row does not see: -inf
             tmem_wait_ld(x);
             if (some) {
               const float lv = b ? lvs.y : lvs.x;
@@ -302,8 +303,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
             add_l = top = 0.f;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              uint32_t x[32];
-              record(b, x);
+              if (b) tmem_ld32(tS + 64 * buf + 32, x);
+              record(b);
               const float lv = b ? lvs.y : lvs.x;
               const bool here = lv == lv;
               const float f1 = here ? (b ? ks.y : ks.x) * qs : 1.f, add1 = here ? lv - at : 0.f;
@@ -331,8 +332,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               float mo = -CUDART_INF_F;
 #pragma unroll 1
               for (int b = 0; b < 2; ++b) {
-                uint32_t x[32];
-                record(b, x);
+                if (b) tmem_ld32(tS + 64 * buf + 32, x);
+                record(b);
                 float m1 = -CUDART_INF_F;
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) m1 = fmaxf(m1, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
@@ -361,11 +362,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
                 }
               }
               first = false;
+              tmem_ld32(tS + 64 * buf, x);
             }
             pass(ref == -CUDART_INF_F ? 0.f : ref);
             if (!first) break;
             up = !(top <= PT_TOP) || (ref == -CUDART_INF_F && lim >= 0);
             if (!__any_sync(0xffffffffu, up)) break;
+            tmem_ld32(tS + 64 * buf, x);
           }
           if (!ok) break;
           l += add_l;
