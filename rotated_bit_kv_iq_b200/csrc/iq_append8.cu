@@ -5,8 +5,8 @@
 // of the tokens that were there if the scale grew; writes the new tokens' codes.  Powers of two
 // (e4m3) and scales of 8 significant bits (int8) make every quotient below correctly rounded, so that
 // the result does not depend on how the tokens were split over calls, apart from that re-rounding.
-// 512 B in and 257 B out for each token and kv head: 32768 tokens of 8 kv heads, bf16 to int8, in 53 us, 3.8 TB/s, bound by
-// the quotients' instructions; one token of 16 sequences in 6, a chain of dependent loads.
+// Bound by memory, 512 B in and 257 B out for each token and kv head: 32768 tokens of 8 kv heads, bf16 to int8, in 33 us,
+// 94% of the copy rate; one token of 16 sequences in 6, a chain of dependent loads.
 #include <math_constants.h>
 
 #include <type_traits>
@@ -15,7 +15,7 @@
 
 namespace iq {
 
-constexpr int AP8_WARPS = 8;
+constexpr int AP8_WARPS = 4;
 
 struct Append8Args {
   View8 v;
@@ -44,8 +44,8 @@ __device__ __forceinline__ float scale_for(uint32_t amax) {
 //   e4m3: the product with a power of two is exact, the conversion the one rounding.
 //   int8: q = x (1 / s), its remainder x - q s and q + remainder (1 / s), each rounded once, give the correctly rounded
 //   quotient (Markstein, 1990: 1 / s correctly rounded, q within one unit in the last place); adding 1.5 2^23 rounds that
-//   to the nearest integer, ties to even, in the low byte.  (The compiler's division for each value: 90 us for the 32K
-//   prompt; the nearest integer to x (1 / s) and a branch for ties: 57; this: 53.)
+//   to the nearest integer, ties to even, in the low byte.  (The compiler's division for each value took 1.7 times as long
+//   for the whole call.)
 template <int CODE, bool ODD>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv) {
   float y[8];
@@ -68,10 +68,14 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, flo
           : "f"(y[4 * h] * inv), "f"(y[4 * h + 1] * inv), "f"(y[4 * h + 2] * inv), "f"(y[4 * h + 3] * inv));
   } else {
     uint32_t c[8];
+    const uint64_t inv2 = f2(inv, inv), neg2 = f2(-scale, -scale), magic2 = f2(kMagicF, kMagicF);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float q = __fmul_rn(y[k], inv);
-      c[k] = round_low_bits(__fmaf_rn(__fmaf_rn(-q, scale, y[k]), inv, q));
+    for (int k = 0; k < 8; k += 2) {  // two values an instruction
+      const uint64_t x2 = f2(y[k], y[k + 1]), q = mul2(x2, inv2);
+      float a, b;
+      f2s(add2(fma2(fma2(q, neg2, x2), inv2, q), magic2), a, b);
+      c[k] = __float_as_uint(a);
+      c[k + 1] = __float_as_uint(b);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -82,26 +86,22 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, flo
 
 // Eight values of one row as float32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float f[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void widen8(const uint4& u, float f[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = a.x;
-        f[2 * i + 1] = a.y;
-      } else {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    } else {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+}
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ uint32_t finite_magnitude(float x) {
   const uint32_t a = __float_as_uint(x) & 0x7FFFFFFFu;
@@ -143,24 +143,49 @@ __global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) 
   const int lo = (int)(first - t0), hi = (int)(end - t0);  // the new tokens' rows
   const T* const src = x + ((long long)b * a.n_new + (t0 - start)) * stride + head * D + 8 * c8;
 
-  // Two passes over the rows, the second from L1 (the rows in registers: 104 of them, code without loops, and 59 us for the
-  // 32K prompt).  First the largest magnitude, of 16-bit types two at a time.
+  // f(i) of the rows 2 i + odd that are new.
+  const bool all = lo == 0 && hi == TILE_TOKENS;
+  auto each = [&](auto f) {
+    if (all) {
+#pragma unroll 8
+      for (int i = 0; i < TILE_TOKENS / 2; ++i) f(i);
+    } else {
+#pragma unroll 1
+      for (int i = lo >> 1; 2 * i + odd < hi; ++i)
+        if (2 * i + odd >= lo) f(i);
+    }
+  };
+  // Two passes over the rows.  A warp's rows of a 16-bit type, 8 KB, are copied to shared memory, all of them in flight at
+  // once; a lane reads back what it copied.  (Loads to registers, and from L1 again, which 40 warps' rows do not fit: 53 us
+  // for the 32K prompt.)  First the largest magnitude, of 16-bit types two at a time.
   constexpr bool WIDE = sizeof(T) == 4;
+  __shared__ uint4 s_rows[WIDE ? 1 : AP8_WARPS][WIDE ? 1 : TILE_TOKENS * D / 8];
+  uint4* const held = s_rows[WIDE ? 0 : threadIdx.x >> 5] + (WIDE ? 0 : lane);
+  auto get = [&](int i, float f[8]) {
+    if constexpr (WIDE) {
+      const float4* const p = reinterpret_cast<const float4*>(src + (2 * i + odd) * stride);
+      const float4 a = __ldg(p), b = __ldg(p + 1);
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+      widen8<T>(held[32 * i], f);
+    }
+  };
   uint32_t amax = 0;
   bool odd_values = false;  // a NaN or an infinity
   if constexpr (!WIDE) {
+    each([&](int i) { copy16_async(held + 32 * i, src + (2 * i + odd) * stride); });
+    asm volatile("cp.async.wait_all;" ::: "memory");
     using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
     auto larger = [](uint32_t x, uint32_t y) {  // of two pairs of magnitudes; NaN wins
       const T2 z = __hmax2_nan(*reinterpret_cast<const T2*>(&x), *reinterpret_cast<const T2*>(&y));
       return *reinterpret_cast<const uint32_t*>(&z);
     };
     uint32_t m = 0;
-#pragma unroll 8
-    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
-      if (r < lo) continue;
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + r * stride));
+    each([&](int i) {
+      const uint4 u = held[32 * i];
       m = larger(m, larger(larger(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu), larger(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu)));
-    }
+    });
     m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
     constexpr bool half = std::is_same<T, __half>::value;
     odd_values = m >= (half ? 0x7C00u : 0x7F80u);
@@ -168,17 +193,15 @@ __global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) 
   }
   if (WIDE || odd_values) {
     amax = 0;
-#pragma unroll 4
-    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
-      if (r < lo) continue;
+    each([&](int i) {
       float f[8];
-      load8(src + r * stride, f);
+      get(i, f);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         odd_values |= !(fabsf(f[k]) < CUDART_INF_F);
         amax = max(amax, finite_magnitude(f[k]));
       }
-    }
+    });
     odd_values = __any_sync(0xffffffffu, odd_values);
     amax = __reduce_max_sync(0xffffffffu, amax);
   }
@@ -208,13 +231,12 @@ __global__ void __launch_bounds__(AP8_WARPS * 32) append8_kernel(Append8Args a) 
     }
   }
   auto write = [&](auto odd_c) {
-#pragma unroll 4
-    for (int r = (lo & ~1) + odd; r < hi; r += 2) {
-      if (r < lo) continue;
+    each([&](int i) {
       float f[8];
-      load8(src + r * stride, f);
-      *reinterpret_cast<uint2*>(rows + chunk8(r, c8 >> 1) + 8 * (c8 & 1)) = quantise8<CODE, decltype(odd_c)::value>(f, scale, inv);
-    }
+      get(i, f);
+      *reinterpret_cast<uint2*>(rows + chunk8(2 * i + odd, c8 >> 1) + 8 * (c8 & 1)) =
+          quantise8<CODE, decltype(odd_c)::value>(f, scale, inv);
+    });
   };
   if (odd_values) write(std::true_type());
   else write(std::false_type());

@@ -7,7 +7,8 @@
 //   O += P V        128 x 128 x 64, P in tensor memory (binary16, over S's own columns), V in shared memory as it lies in
 //                   the cache: rows of coordinates (N-major operand)
 // Each tile has two S buffers: while the softmax is at one half-step's scores the tensor core adds the P of the half-step
-// before and makes the scores of the one after.  (One buffer of 128 keys a tile: 318 us on the 2048-token chunk.)
+// before and makes the scores of the one after.  (One buffer of 128 keys a tile: 334 us on the 2048-token
+// chunk, 265 so.)
 // The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and the V
 // scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is the first half-step's maximum
 // of s + log2 v, and follows only once the p' of a half-step add up to more than 2^15: O is then rescaled in tensor memory,
@@ -20,9 +21,10 @@
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
 // and 18 issue the two tiles' MMAs, 17 finds the records and their scales.
 //
-// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 296-311 us, 773-813 TFLOP/s, 46-49% of cuBLAS's bf16
-// rate.  Of a step's 5,200 cycles the MMAs take 2,500 (a 64-key score product runs at 64% of the MMA rate: 50 cycles for
-// 32) and the softmax, on its own, 2,900, bound by the exponentials (MUFU); the two overlap to less than half.
+// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 265 us, 907 TFLOP/s, 54% of cuBLAS's bf16 rate.  Of a
+// step's 4,600 cycles the MMAs take 2,500 (a 64-key score product, fed from shared memory, runs at 64% of the MMA rate: 50
+// cycles for 32), the exponentials (MUFU) 2,050, instruction issue 2,100 a scheduler; the rest is latency of the softmax
+// warps, two a scheduler.
 #pragma once
 #include <algorithm>
 
@@ -36,7 +38,8 @@ constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
 constexpr int PT_THREADS = 640;
 // registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96.  With 64
-// for the MMA warp, which then spills, the 2048-token chunk takes 303 us instead of 296.
+// for the MMA warp, which then spills, the 2048-token chunk takes 303 us instead of 296; 120 / 80 / 80 and 104 / 88 / 96 for the three: 273 and 269
+// instead of 265.
 constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
