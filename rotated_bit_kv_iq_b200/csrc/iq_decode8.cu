@@ -2,11 +2,11 @@
 // blocks of up to eight rows.
 //
 // The work is the list of 32-token tiles of all (entry, kv head) groups, an entry being a sequence or a block of its query
-// tokens; CTA c of N takes tiles [c T / N, (c + 1) T / N), whatever the mix of lengths.  Its warps take the tiles of each
+// tokens; CTA c of N takes an N-th of them, whatever the mix of lengths, a group's first tile counting for more.  Its warps take the tiles of each
 // group's segment in turn, each through a ring of its own of two bulk-copied tile records: twelve warps, three a scheduler,
-// at 168 registers.  On a layer of 16 sequences of 2K to 32K tokens, 32 query and 8 kv heads: 92-96 us, 77-79% of the copy
-// rate; 105 with eight warps (197 registers); 121 with sixteen (128 registers, which do not hold a tile's work) on one ring
-// of 26 records.  A segment that is a whole group is finished at once; the others
+// at 168 registers.  On a layer of 16 sequences of 2K to 32K tokens, 32 query and 8 kv heads: 82 us, 89% of the copy
+// rate.  (Before groups had a lead: 94; 105 with eight warps of 197 registers; 121 with sixteen, whose 128 registers do not
+// hold a tile's work, on one ring of 26 records.)  A segment that is a whole group is finished at once; the others
 // leave a partial (m, mo, l, O), and the last CTA of a group to arrive merges the group's partials in a fixed order, so
 // that results do not depend on who is last.  Bound by memory: 257 B for each (token, kv head).
 #include <algorithm>
@@ -19,6 +19,10 @@ constexpr int D8_WARPS = 12;
 constexpr int D8_THREADS = 32 * D8_WARPS;
 constexpr int D8_NB = 2;                                       // tile records in a warp's ring
 constexpr int D8_UNCUT = 2 * D8_WARPS;                         // tiles of a group that is not cut
+// What a group costs beside its tiles (its queries, an empty ring, the warps' merge), in tiles, about 6 us: without it the
+// CTAs that get many short groups are the last (the 16-sequence layer: CTAs of 63 to 90 us; with it 62 to 80).  Leads of
+// 0, 8, 16, 24, 32, 48, 64: 96, 90, 88, 84, 82, 83, 84 us.
+constexpr int D8_LEAD = 32;
 constexpr int D8_SMEM = D8_WARPS * D8_NB * TILE8_BYTES;        // (at a segment's end: the warps' value sums)
 static_assert(D8_WARPS * A8_ROWS * D * 4 <= D8_SMEM, "value sums in the rings' place");
 
@@ -66,6 +70,9 @@ __device__ __forceinline__ int d8_tiles(const Decode8Args& a, int e) {
   return (d8_entry<CHUNK>(a, e).ctx + TILE_TOKENS - 1) / TILE_TOKENS;
 }
 
+// The same with the lead, for the sharing of the work.
+__device__ __forceinline__ int d8_cost(int tiles) { return tiles ? tiles + D8_LEAD : 0; }
+
 // Final value of one row of the group: lane holds sums of coordinates 4 lane ..
 __device__ __forceinline__ void finish_row8(const Decode8Args& a, size_t row, float M, float MO, float L, float4 o) {
   const float f = L > 0.f ? fast_exp2(MO - M) / L : (L == L ? 0.f : L);
@@ -79,7 +86,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __shared__ float sml[D8_WARPS][A8_ROWS][4];
   __shared__ long long s_scan[D8_WARPS];
   __shared__ int s_most[D8_WARPS];
-  __shared__ int s_start[2];  // the CTA's first entry, and the tiles before it within all kv heads
+  __shared__ int s_start[2];  // the CTA's first entry, and the cost before it within all kv heads
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int Hkv = a.v.n_kv_heads, G = a.g_real, c = blockIdx.x;
@@ -91,13 +98,13 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __syncwarp();
   pdl_wait();
 
-  // ---- plan: total tiles, this CTA's range, the sequence that it starts in
+  // ---- plan: total cost, this CTA's range, the sequence that it starts in.  A group is D8_LEAD places and its tiles.
   const int E = a.batch * a.n_blk, per = (E + D8_THREADS - 1) / D8_THREADS, e0 = min(E, tid * per), e1 = min(E, e0 + per);
   long long mine = 0;
   int most = 0;  // tiles of an entry
   for (int e = e0; e < e1; ++e) {
     const int n = d8_tiles<CHUNK>(a, e);
-    mine += n;
+    mine += d8_cost(n);
     most = max(most, n);
   }
   most = __reduce_max_sync(0xffffffffu, most);
@@ -121,9 +128,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   // the CTAs that share the tiles: none without one, and no more than give every warp one
   const int N = (int)min((long long)gridDim.x, max(1ll, (total + D8_WARPS - 1) / D8_WARPS));
   const long long lo = c < N ? c * total / N : total, hi = c < N ? (c + 1) * total / N : total;
-  long long acc = before;  // tiles of all groups before entry e
+  long long acc = before;  // cost of all groups before entry e
   for (int e = e0; e < e1 && acc <= lo; ++e) {
-    const long long n = (long long)Hkv * d8_tiles<CHUNK>(a, e);
+    const long long n = (long long)Hkv * d8_cost(d8_tiles<CHUNK>(a, e));
     if (lo < hi && lo < acc + n) {
       s_start[0] = e;
       s_start[1] = (int)(lo - acc);
@@ -152,7 +159,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   // is nothing to merge (a 512-token layer of two kv heads: 9 us a call, 15 cut).
   const bool uncut = most <= D8_UNCUT;
   if (!uncut && lo >= hi) return;
-  int e = 0, kvh = 0, nt = 0, tile0 = 0;
+  int e = 0, kvh = 0, nt = 0, at = 0;  // nt: the group's tiles; at: where in the group's places the segment starts
   D8Entry x = {};
   long long pos = lo, gi = c;
   auto take = [&]() {  // uncut: the next group that has tiles, from gi on; whether there is one
@@ -172,8 +179,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     e = s_start[0];
     x = d8_entry<CHUNK>(a, e);
     nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
-    kvh = s_start[1] / nt;
-    tile0 = s_start[1] % nt;
+    kvh = s_start[1] / d8_cost(nt);
+    at = s_start[1] % d8_cost(nt);
     more = true;
   }
   uint32_t used = 0;  // of this warp's ring, so far
@@ -186,7 +193,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   };
   while (more) {
     // ---- one segment: tiles [tile0, tile1) of group (e, kvh)
-    const int tile1 = uncut ? nt : (int)min((long long)nt, tile0 + (hi - pos));
+    const int end = uncut ? d8_cost(nt) : (int)min((long long)d8_cost(nt), at + (hi - pos));
+    const int tile0 = max(0, at - D8_LEAD), tile1 = end - D8_LEAD;
+    if (tile1 <= tile0) break;  // the range ends before the group's first tile
     const int mine = ok && tile1 - tile0 > warp ? (tile1 - tile0 - warp + D8_WARPS - 1) / D8_WARPS : 0;  // this warp's
     auto issue = [&](int j) {  // the warp's j-th tile of the segment; whether it has a page
       const int tile = tile0 + warp + D8_WARPS * j, idx = tile / page_tiles;
@@ -221,9 +230,9 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       if (!ok) break;
       uint8_t* const t = ring + n % D8_NB * TILE8_BYTES;
       if ((have >> (j % D8_NB)) & 1) {
-        const int at = (tile0 + warp + D8_WARPS * j) * TILE_TOKENS;
-        if (x.ctx - at < TILE_TOKENS) clear_v_rows8(t, x.ctx - at);
-        tile8<CODE, FEW>(t, seen - at, qa, qs, r);
+        const int first = (tile0 + warp + D8_WARPS * j) * TILE_TOKENS;
+        if (x.ctx - first < TILE_TOKENS) clear_v_rows8(t, x.ctx - first);
+        tile8<CODE, FEW>(t, seen - first, qa, qs, r);
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this slot's reads before the next copy into it
@@ -263,16 +272,16 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       }
     }
     if (!whole) {
-      // contributors: the CTAs whose ranges meet the group's tiles [g0, g1)
-      const long long g0 = pos - tile0, g1 = g0 + nt;
-      // the CTA of tile x is the last c with c total / N <= x
+      // contributors: the CTAs whose ranges meet the tiles of the group's places [g0, g1)
+      const long long g0 = pos - at, g1 = g0 + d8_cost(nt);
+      // the CTA of place x is the last c with c total / N <= x
       auto cta_of = [&](long long x) {
         long long k = x * N / total;
         while ((k + 1) * total / N <= x) ++k;
         while (k * total / N > x) --k;
         return (int)k;
       };
-      const int c0 = cta_of(g0), c1 = cta_of(g1 - 1);
+      const int c0 = cta_of(g0 + D8_LEAD), c1 = cta_of(g1 - 1);
       __threadfence();
       __syncthreads();
       if (tid == 0) {
@@ -335,8 +344,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       more = take();
       continue;
     }
-    pos += tile1 - tile0;
-    tile0 = 0;
+    pos += end - at;
+    at = 0;
     more = pos < hi;
     if (more && ++kvh == Hkv) {
       kvh = 0;
