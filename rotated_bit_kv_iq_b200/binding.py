@@ -422,16 +422,23 @@ def _bad(fn, what):
     raise ValueError(f"{fn}: {what}")
 
 
-def _dtype(fn, t):
-    import torch
+_dtypes = {}  # torch's number types -> the library's; and "i32", "f64"
 
-    if t.dtype == torch.float16:
-        return IQ_F16
-    if t.dtype == torch.bfloat16:
-        return IQ_BF16
-    if t.dtype == torch.float32:
-        return IQ_F32
-    _bad(fn, f"float16, bfloat16 or float32 wanted, got {t.dtype}")
+
+def _types():
+    if not _dtypes:
+        import torch
+
+        _dtypes.update({torch.float16: IQ_F16, torch.bfloat16: IQ_BF16, torch.float32: IQ_F32, "i32": torch.int32,
+                        "f64": torch.float64, "torch": torch})
+    return _dtypes
+
+
+def _dtype(fn, t):
+    d = _types().get(t.dtype)
+    if d is None:
+        _bad(fn, f"float16, bfloat16 or float32 wanted, got {t.dtype}")
+    return d
 
 
 def _plain(fn, name, t, dev, dtype, shape):
@@ -443,9 +450,7 @@ def _plain(fn, name, t, dev, dtype, shape):
 
 
 def _i32(fn, name, t, dev, n):
-    import torch
-
-    return _plain(fn, name, t, dev, torch.int32, (n,))
+    return _plain(fn, name, t, dev, _types()["i32"], (n,))
 
 
 def _bytes(fn, name, t, dev):
@@ -460,8 +465,7 @@ _fns = {}  # the library's functions by name
 
 def _run8(fn, dev, stream, *args):
     """The C call `fn` on device `dev`, its stream last."""
-    import torch
-
+    torch = _types()["torch"]
     if dev < 0:
         _bad(fn, "CUDA tensors wanted")
     if stream is None:
@@ -539,16 +543,18 @@ def iq_append8(cache, layer, k, v, start_pos, n_valid=None, stream=None):
     _batch8(fn, cache, batch)
     if batch == 0 or n == 0:
         return
-    strides = []
+    strides, shape = [], (batch, n, cache.n_kv_heads, HEAD_DIM)
     for t in (k, v):
         if t is None:
             strides.append(0)
             continue
-        stride = t.stride(1) if n > 1 else t.stride(0) if batch > 1 else 0
-        if (t.dtype != x.dtype or t.get_device() != dev or t.shape != (batch, n, cache.n_kv_heads, HEAD_DIM)
-                or t.stride(3) != 1 or (t.shape[2] > 1 and t.stride(2) != HEAD_DIM)
-                or (batch > 1 and t.stride(0) != n * stride)
-                or (batch * n > 1 and stride < cache.n_kv_heads * HEAD_DIM)):  # (a broadcast tensor's 0)
+        ok, stride = t.dtype == x.dtype and t.get_device() == dev and t.shape == shape, 0  # 0: contiguous rows
+        if ok and not t.is_contiguous():
+            st = t.stride()
+            stride = st[1] if n > 1 else st[0] if batch > 1 else 0
+            ok = (st[3] == 1 and (shape[2] == 1 or st[2] == HEAD_DIM) and (batch == 1 or st[0] == n * stride)
+                  and (batch * n == 1 or stride >= shape[2] * HEAD_DIM))  # (a broadcast tensor's is 0)
+        if not ok:
             _bad(fn, f"[{batch}][{n}][{cache.n_kv_heads}][128] tensors of one type, with contiguous heads and equally "
                      f"distant tokens, on cuda:{dev} wanted, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
         strides.append(stride)
@@ -629,23 +635,24 @@ def _rope_side(fn, name, x, y, dtype, dev, n):
             _bad(fn, f"{name} and {name}_out belong together")
         return None, 0, None, 0, 0
     heads = x.shape[1] if x.dim() == 3 else 0
-    for t in (x, y):
-        if (t.dtype != dtype or t.get_device() != dev or t.shape != (n, heads, HEAD_DIM) or t.stride(2) != 1
-                or (heads > 1 and t.stride(1) != HEAD_DIM)
-                or (n > 1 and t.stride(0) < heads * HEAD_DIM)):  # (a broadcast tensor's 0)
+    shape, strides = (n, heads, HEAD_DIM), []
+    for t in (x,) if y is x else (x, y):
+        ok, stride = t.dtype == dtype and t.get_device() == dev and t.shape == shape, 0  # 0: contiguous rows
+        if ok and not t.is_contiguous():
+            st = t.stride()
+            stride = st[0] if n > 1 else 0
+            ok = st[2] == 1 and (heads == 1 or st[1] == HEAD_DIM) and (n == 1 or stride >= heads * HEAD_DIM)  # (broadcast: 0)
+        if not ok:
             _bad(fn, f"{name}: [{n}][heads][128] tensors of one type with contiguous heads on cuda:{dev} wanted, got "
                      f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    if n < 2:
-        return x.data_ptr(), 0, y.data_ptr(), 0, heads
-    return x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), heads
+        strides.append(stride)
+    return x.data_ptr(), strides[0], y.data_ptr(), strides[-1], heads
 
 
 def iq_rope(q, k, positions, freq, q_out=None, k_out=None, layout="half", mscale=1.0, inverse=False, stream=None):
     """q, k: fp16, bf16 or fp32 [n_tokens][heads][128] (either may be None), rows as far apart as they may be;
     q_out, k_out: where the results go, by default q and k themselves; positions: int32 [n_tokens]; freq:
     float64 [rotary_dim/2] (iq_rope_frequencies)."""
-    import torch
-
     fn = "iq_rope"
     x = q if q is not None else k
     if x is None:
@@ -658,7 +665,7 @@ def iq_rope(q, k, positions, freq, q_out=None, k_out=None, layout="half", mscale
     a = _rope_side(fn, "q", q, q if q_out is None else q_out, x.dtype, dev, n)
     b = _rope_side(fn, "k", k, k if k_out is None else k_out, x.dtype, dev, n)
     _run8(fn, dev, stream, *a[:4], *b[:4], _dtype(fn, x), n, a[4], b[4], 2 * pairs, ROPE_LAYOUTS.get(layout, layout),
-          _i32(fn, "positions", positions, dev, n), _plain(fn, "freq", freq, dev, torch.float64, (pairs,)), mscale,
+          _i32(fn, "positions", positions, dev, n), _plain(fn, "freq", freq, dev, _types()["f64"], (pairs,)), mscale,
           1 if inverse else 0)
 
 

@@ -2,13 +2,14 @@
 // blocks of up to eight rows.
 //
 // The work is the list of 32-token tiles of all (entry, kv head) groups, an entry being a sequence or a block of its query
-// tokens; CTA c of N takes an N-th of them, whatever the mix of lengths, a group's first tile counting for more.  Its warps take the tiles of each
-// group's segment in turn, each through a ring of its own of two bulk-copied tile records: twelve warps, three a scheduler,
-// at 168 registers.  On a layer of 16 sequences of 2K to 32K tokens, 32 query and 8 kv heads: 82 us, 89% of the copy
-// rate.  (Before groups had a lead: 94; 105 with eight warps of 197 registers; 121 with sixteen, whose 128 registers do not
-// hold a tile's work, on one ring of 26 records.)  A segment that is a whole group is finished at once; the others
-// leave a partial (m, mo, l, O), and the last CTA of a group to arrive merges the group's partials in a fixed order, so
-// that results do not depend on who is last.  Bound by memory: 257 B for each (token, kv head).
+// tokens; CTA c of N takes an N-th of them, whatever the mix of lengths, a group's first tile counting for more.  Its warps
+// take the tiles of each group's segment in turn, each through a ring of its own of two bulk-copied tile records: twelve
+// warps, three a scheduler, at 168 registers.  A segment that is a whole group is finished at once; the others leave a
+// partial (m, mo, l, O), and the last CTA of a group to arrive merges the group's partials in a fixed order, so that results
+// do not depend on who is last.
+// Bound by memory, 257 B for each (token, kv head).  A layer of 16 sequences of 2K to 32K tokens, 32 query and 8 kv heads:
+// 82-84 us, 87-89% of the copy rate.  (Before groups counted for more than their tiles: 94; 105 with eight warps of 197
+// registers; 121 with sixteen, whose 128 registers do not hold a tile's work, on one ring of 26 records.)
 #include <algorithm>
 
 #include "iq_attend8.cuh"
