@@ -5,8 +5,8 @@
 // of the tokens that were there if the scale grew; writes the new tokens' codes.  Powers of two
 // (e4m3) and scales of 8 significant bits (int8) make every quotient below correctly rounded, so that
 // the result does not depend on how the tokens were split over calls, apart from that re-rounding.
-// Bound by memory, 512 B in and 257 B out for each token and kv head: 32768 tokens of 8 kv heads, bf16 to int8, in 33 us,
-// 94% of the copy rate; one token of 16 sequences in 6, a chain of dependent loads.
+// Bound by memory, 512 B in and 257 B out for each token and kv head: 32768 tokens of 8 kv heads, bf16 to int8, in 33 to
+// 36 us, 87-94% of the copy rate; one token of 16 sequences in 6, a chain of dependent loads.
 #include <math_constants.h>
 
 #include <type_traits>

@@ -21,7 +21,8 @@
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
 // and 18 issue the two tiles' MMAs, 17 finds the records and their scales.
 //
-// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 265 us, 907 TFLOP/s, 54% of cuBLAS's bf16 rate.  Of a
+// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 265 us back to back, 907 TFLOP/s, 54% of cuBLAS's
+// bf16 rate; 291 with the caches flushed between calls.  Of a
 // step's 4,600 cycles the MMAs take 2,500 (a 64-key score product, fed from shared memory, runs at 64% of the MMA rate: 50
 // cycles for 32), the exponentials (MUFU) 2,050, instruction issue 2,100 a scheduler; the rest is latency of the softmax
 // warps, two a scheduler.
@@ -37,9 +38,8 @@ constexpr int PT_TILE = 128;  // rows of a tile: the MMA's M
 constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
 constexpr int PT_THREADS = 640;
-// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96.  With 64
-// for the MMA warp, which then spills, the 2048-token chunk takes 303 us instead of 296; 120 / 80 / 80 and 104 / 88 / 96 for the three: 273 and 269
-// instead of 265.
+// registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96.  The
+// 2048-token chunk takes 265 us so, 273 with 120 / 80 / 80, 269 with 104 / 88 / 96; the MMA warps spill with 64.
 constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
