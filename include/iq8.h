@@ -20,6 +20,8 @@ extern "C" {
 #define IQ_DEVERR_SEQ 32u /* page operation: sequence id outside the table, listed twice, or not empty */
 #define IQ_DEVERR_NOPAGE 64u /* page operation: no free page left, or a sequence longer than its table row */
 
+#define IQ_DEVERR_RANGE 128u /* prefill: V scales of a sequence too far apart (those rows may be wrong) */
+
 /* ------------------------------------------------------------------ the 8-bit cache
  * A cache whose K and V are held in 8 bits, unrotated (no block rotation), with one scale for each block of 32 tokens
  * and kv head (K and V apart).  The calls beside it have the conventions above (asynchronous on the
@@ -103,6 +105,8 @@ size_t iq_prefill8_workspace_size(int32_t batch, int32_t n_tokens, int32_t n_q_h
  *   n_valid_dev    : int32 [batch] or NULL: only the first n_valid[b] tokens (clamped to 0..n_tokens,
  *                    flagged) are there; the rows of `out` behind them are left as they were.
  *   start_pos      : values outside [0, max_ctx - n_valid[b]] are clamped and flagged.
+ * With 16-bit queries the V scales of a sequence's blocks of a kv head are to lie within a factor of 2^104 of
+ * each other (a block of zeros has 2^-100); what is farther apart is flagged (IQ_DEVERR_RANGE).
  * Other arguments as for iq_decode8_attention.  At most 2^27 kv heads' tokens (batch Hkv n_tokens), and 2^31
  * steps of 128 keys by the blocks of 256 / G tokens (IQ_ERR_UNSUPPORTED above). */
 iq_status iq_prefill8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,

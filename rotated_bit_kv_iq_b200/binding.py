@@ -30,6 +30,7 @@ IQ_DEVERR_TIMEOUT = 8
 IQ_DEVERR_WORKSPACE = 16
 IQ_DEVERR_SEQ = 32
 IQ_DEVERR_NOPAGE = 64
+IQ_DEVERR_RANGE = 128
 IQ_ROT_ISO = 0
 IQ_ROT_QUAT = 1
 IQ_ROT_PLANAR = 2

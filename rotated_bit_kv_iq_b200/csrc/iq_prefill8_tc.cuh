@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
     if (warp == 17) {
       // ==== where the records of each step are, and their scales; lane b < 4: record b
       const int page_tiles = a.v.page_size / TILE_TOKENS;
-      float base = 0.f;
+      float base = 0.f, least = CUDART_INF_F, most = -CUDART_INF_F;  // of the segment's log2 of V scales
       bool more = true;
       int step = s.k0;
       for (uint32_t n = 0; more; ++n) {
@@ -508,6 +508,23 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           const float first = __shfl_sync(0xffffffffu, lv, m ? __ffs(m) - 1 : 0);
           base = m ? first : 0.f;
         }
+        // p' below 2^-126 is 0, and with it the key's share of the row's sum: of scales within 2^104 of each other (a block
+        // of zeros has 2^-100) only keys of weights below 2^-22 are lost so
+        if (step == s.k0) {
+          least = CUDART_INF_F;
+          most = -CUDART_INF_F;
+        }
+        if (there) {
+          least = fminf(least, lv);
+          most = fmaxf(most, lv);
+        }
+        float up = most, down = least;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+          down = fminf(down, __shfl_xor_sync(0xffffffffu, down, o));
+        }
+        if (lane == 0 && up - down > 104.f && a.v.status) atomicOr(a.v.status, IQ_DEVERR_RANGE);
         if (lane < 4) {
           const int i = 4 * (n & 7) + lane;
           reinterpret_cast<float*>(smem + SM::ks)[i] = sc.x;

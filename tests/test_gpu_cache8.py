@@ -455,6 +455,30 @@ def test_prefill_scales_far_apart():
         _check_prefill(h, q, o, [0], [250], dtype, stride=7)
 
 
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+def test_prefill_scales_at_the_ends_of_their_range(code):
+    """V scales 2^96 apart, or blocks of zeros, are within what 16-bit queries take; farther ones are flagged.  Decode
+    takes any."""
+    for up, down, flag in ((48, 48, 0), (0, None, 0), (70, 70, B.IQ_DEVERR_RANGE)):
+        h = Held(1, 1, 256, 1, code, contiguous=True)
+        k, v = _tokens(92, (1, 256, 1, 128), F32), _tokens(93, (1, 256, 1, 128), F32)
+        v[:, 32:64] *= 2.0 ** up
+        v[:, 96:160] *= 0.0 if down is None else 2.0 ** -down
+        if down is None:
+            v[:, :32] = 0.0
+        k[:, 32:64] *= 8.0  # scores far above and far below the others'
+        h.append(k, v, [0])
+        q = torch.randn((1, 250, 2, 128), generator=torch.Generator().manual_seed(4)).to(BF16)
+        o = _prefill(h, q, [0], 256)
+        if not flag:
+            _check_prefill(h, q, o, [0], [250], BF16, stride=7)
+        assert h.c.status.item() == flag
+        h.c.status.zero_()
+        kk, vv = h.kv(0, 0, 256)
+        _check_rows(_decode(h, q[:, 0].to(F32), [256], 256)[0], q[0, 0].double().numpy(), kk[None], vv[None], 128 ** -0.5, F32)
+        assert h.c.status.item() == 0
+
+
 # ------------------------------------------------------------------------------- streams, graphs, one run
 def test_calls_on_another_stream_and_in_graphs():
     """append -> decode captured into two graphs that share a workspace, replayed in turn on a side stream."""
