@@ -10,10 +10,14 @@
 // before and makes the scores of the one after.  (One buffer of 128 keys a tile: 334 us on the 2048-token
 // chunk, 265 so.)
 // The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and the V
-// scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is the first half-step's maximum
-// of s + log2 v, and follows only once the p' of a half-step add up to more than 2^15: O is then rescaled in tensor memory,
-// rarely.  p' is one binary16 number (relative 2^-11, no more than the output's own rounding to 16 bits); all sums are
-// float32.
+// scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is 8 below the first half-step's
+// maximum of s + log2 v, and follows only once the p' of a half-step add up to more than 65504: O is then rescaled in tensor
+// memory, rarely.
+// p' is one binary16 number, all sums are float32.  A weight is rounded by 2^-11 of itself, as the output is by its own
+// type: the error of the fp16 chunk against 64 bits is 2.6e-4 for the 2.1e-4 of the output's rounding alone (two terms, as
+// for float32 queries, would double the products P V).  2^8 for the largest p' of the first half-step leaves binary16's normal
+// numbers for weights down to 2^-22 of the largest times V scale that the row has met, and its steps of 2^-24 below: a key
+// is off by at most 2^-33 of that, 131072 keys by 2^-16.
 //
 // Work: the list of (block, step) over all blocks is cut into equal runs, one per CTA (one CTA per SM), so that neither
 // causal lengths nor ragged batches nor a number of blocks off the number of SMs leave SMs idle.  A block cut by a run's
@@ -43,7 +47,10 @@ constexpr int PT_THREADS = 640;
 constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
-constexpr float PT_TOP = 32768.f;  // 2^15: the most that p' of a half-step add up to (binary16 reaches 2^16)
+constexpr float PT_TOP = 65504.f;  // the most that p' of a half-step add up to: binary16's largest number
+// log2 of the largest p' of a half-step that sets ref (64 of them are below PT_TOP).  The 2048-token chunk takes 295 us so and
+// 290 with 4, which leaves 12 bits until the next rescaling, not 8; but then 131072 keys are off by 2^-12.
+constexpr float PT_ABOVE = 8.f;
 
 struct PtSmem {
   static constexpr int q = 0;                 // [tile] 128 rows x 128 coordinates
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               add_l = fmaf(s0 + s1, b ? ws.y : ws.x, add_l);
             }
           };
-          // A block's first half-step, and rarely one after it: ref becomes the half-step's maximum first
+          // A block's first half-step, and rarely one after it: ref first goes to PT_ABOVE below the half-step's maximum
           bool up = i == 0;
           for (bool first = true;; first = false) {
             if (__any_sync(0xffffffffu, up)) {
@@ -343,8 +350,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
                 const float lv = b ? lvs.y : lvs.x;
                 if (m1 > -CUDART_INF_F) mo = fmaxf(mo, lv == lv ? fmaf(m1, (b ? ks.y : ks.x) * qs, lv) : m1);
               }
-              const float al = up ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
-              if (up) ref = mo;
+              // (rows that could wait follow too, since O is gone through anyway: fewer times for the warp in all)
+              mo -= PT_ABOVE;
+              const float al = mo > ref ? (ref == -CUDART_INF_F ? 0.f : fast_exp2(ref - mo)) : 1.f;
+              ref = fmaxf(ref, mo);
               if (i > 0) {
                 // O += P V of the half-step before is done: the scores of the next one, or at the end a barrier of its
                 // own, are signalled after it
@@ -509,7 +518,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           base = m ? first : 0.f;
         }
         // p' below 2^-126 is 0, and with it the key's share of the row's sum: of scales within 2^104 of each other (a block
-        // of zeros has 2^-100) only keys of weights below 2^-22 are lost so
+        // of zeros has 2^-100) only keys of weights below 2^-30 are lost so
         if (step == s.k0) {
           least = CUDART_INF_F;
           most = -CUDART_INF_F;
