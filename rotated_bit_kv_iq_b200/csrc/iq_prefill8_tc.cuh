@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
               record(b);
               const float lv = b ? lvs.y : lvs.x;
               const bool here = lv == lv;
-              const float f1 = here ? (b ? ks.y : ks.x) * qs : 1.f, add1 = here ? lv - at : 0.f;
+              // (a row of zeros over a block of zeros: the product may underflow, and 0 times a hidden key's -inf is NaN)
+              const float f1 = here ? fmaxf((b ? ks.y : ks.x) * qs, 1.17549435e-38f) : 1.f, add1 = here ? lv - at : 0.f;
               const uint64_t ff = f2(f1, f1), add = f2(add1, add1);
               uint64_t sum[2] = {0, 0};
 #pragma unroll

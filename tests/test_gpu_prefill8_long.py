@@ -114,7 +114,7 @@ def _check(cache, q, o, start, cnt, scale=128 ** -0.5, rows=48, gone=None, fill=
             tol = mass * (1.5 * es + 2.0 ** -20 + T * 2.0 ** -24 + 2.0 ** -11) + T * 2.0 ** -32 * vtop
             tol = tol + want.abs() * HALF_STEP[q.dtype] + (2.0 ** -25 if q.dtype == F16 else 0.0)
             assert torch.isfinite(got).all(), (b, i)
-            share = ((got - want).abs() / tol).max().item()
+            share = ((got - want).abs() / tol.clamp_min(1e-300)).max().item()  # (values of zeros: neither may be off)
             assert share <= 1.0, (b, i, share)
             used = max(used, share)
     return used
@@ -239,4 +239,45 @@ def test_many_keys_far_below_the_first(dtype, code, down):
     o = _prefill(c, q, [T - n], T, scale=scale)
     assert o.double().min().item() > 0
     _check(c, q, o, [T - n], [n], scale=scale, rows=64)
+    assert c.c.status.item() == 0
+
+
+def _visible_mean(c, b, pos, g):
+    v = c.held(b, pos + 1)[1]
+    return v.mean(1).repeat_interleave(g, 0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("n,start", [(37, 0), (1, 0), (70, 33), (129, 500), (33, 31)])
+def test_zero_queries_over_zero_keys_give_the_mean(dtype, code, n, start):
+    """Rows of zeros, and rows too small to tell from them, over blocks of zeros: every key counts alike.  Chunks that end
+    inside a record of 32 keys, with values and without."""
+    T = start + n
+    for v in (_tokens(20, (1, T, 2, 128)).to(dtype), torch.zeros((1, T, 2, 128), dtype=dtype, device=DEV)):
+        c = Cache(1, 2, 64, 10, code)
+        c.append(torch.zeros((1, T, 2, 128), dtype=dtype, device=DEV), v)
+        for tiny in (0.0, 1e-30 if dtype == BF16 else 6e-8):
+            q = torch.full((1, n, 8, 128), tiny, dtype=dtype, device=DEV)
+            o = _prefill(c, q, [start], 640)
+            assert torch.isfinite(o).all()
+            _check(c, q, o, [start], [n])
+            want = _visible_mean(c, 0, T - 1, 4)
+            assert ((o[0, -1].double() - want).abs() <= 2.0 ** -7 * want.abs() + 2.0 ** -10 * v.double().abs().max()).all()
+        assert c.c.status.item() == 0
+
+
+@pytest.mark.parametrize("dtype,code", [(F16, "s8"), (BF16, "e4m3")])
+def test_zero_blocks_among_others(dtype, code):
+    """Rows of zeros over keys some of whose blocks are zeros, and ordinary rows beside them."""
+    n = 300
+    c = Cache(1, 1, 32, 10, code)
+    k, v = _tokens(21, (1, n, 1, 128)), _tokens(22, (1, n, 1, 128))
+    k[:, 32:96], k[:, 288:] = 0.0, 0.0
+    c.append(k.to(dtype), v.to(dtype))
+    q = _q(23, (1, n, 4, 128), dtype)
+    q[:, ::3] = 0.0
+    q[:, 1::7, 2] = 0.0
+    o = _prefill(c, q, [0], 320)
+    _check(c, q, o, [0], [n], rows=300)
     assert c.c.status.item() == 0
