@@ -50,22 +50,19 @@ template <int CODE, bool ODD>
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, float inv) {
   float y[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = x[k];
-  if (ODD) {  // NaN or infinities among the tile's values
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float top = CODE == IQ_E4M3 ? 448.f : 127.f;
-      y[k] = y[k] == y[k] ? y[k] : 0.f;
-      if (fabsf(y[k]) == CUDART_INF_F) y[k] = copysignf(top * scale, y[k]);
-    }
-  }
+  for (int k = 0; k < 8; ++k) y[k] = !ODD || fabsf(x[k]) < CUDART_INF_F ? x[k] : 0.f;  // ODD: NaN or infinities among them
   uint32_t o[2];
   if constexpr (CODE == IQ_E4M3) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] *= inv;
+      if (ODD && fabsf(x[k]) == CUDART_INF_F) y[k] = copysignf(448.f, x[k]);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       asm("{\n .reg .b16 t, u;\n cvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 u, %4, %3;\n mov.b32 %0, {t, u};\n}\n"
           : "=r"(o[h])
-          : "f"(y[4 * h] * inv), "f"(y[4 * h + 1] * inv), "f"(y[4 * h + 2] * inv), "f"(y[4 * h + 3] * inv));
+          : "f"(y[4 * h]), "f"(y[4 * h + 1]), "f"(y[4 * h + 2]), "f"(y[4 * h + 3]));
   } else {
     uint32_t c[8];
     const uint64_t inv2 = f2(inv, inv), neg2 = f2(-scale, -scale), magic2 = f2(kMagicF, kMagicF);
@@ -76,6 +73,12 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale, flo
       f2s(add2(fma2(fma2(q, neg2, x2), inv2, q), magic2), a, b);
       c[k] = __float_as_uint(a);
       c[k + 1] = __float_as_uint(b);
+    }
+    // (127 scale in an infinity's place would itself be infinite beside float32's largest numbers)
+    if (ODD) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (fabsf(x[k]) == CUDART_INF_F) c[k] = x[k] > 0.f ? 127u : (uint32_t)-127;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
