@@ -90,7 +90,8 @@ size_t iq_decode8_workspace_size(int32_t batch, int32_t n_q_heads, int32_t n_kv_
  * ctx_len, max_ctx, workspace, batch <= 2048 and the group size of 1..8 as for iq_decode_attention:
  * max_ctx at most 2^30, and 2^35 / Hkv (IQ_ERR_UNSUPPORTED above);
  * ctx_len 0 gives a zero row, values outside [0, max_ctx] are clamped and flagged (IQ_DEVERR_CTX).
- * Tokens of a page outside the pool are left out and flagged (IQ_DEVERR_PAGE). */
+ * Tokens of a page outside the pool, and of a record in which nothing was written (a K or V scale that is no positive
+ * finite number), are left out and flagged (IQ_DEVERR_PAGE). */
 iq_status iq_decode8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,
                                int32_t n_q_heads, const int32_t* ctx_len_dev, int32_t max_ctx, float scale,
                                void* out_dev, void* workspace_dev, size_t workspace_bytes, iq_stream_t stream);

@@ -31,6 +31,11 @@ __device__ __forceinline__ int find_page8(const View8& v, int b, long long pos, 
   return page;
 }
 
+// Whether a record's K and V scales are ones that an append leaves, positive finite numbers: otherwise it holds nothing.
+__device__ __forceinline__ bool written8(float2 scales) {
+  return __float_as_uint(scales.x) - 1u < 0x7F7FFFFFu && __float_as_uint(scales.y) - 1u < 0x7F7FFFFFu;
+}
+
 // Byte offset of 16-byte chunk c of row s within a tile's 4096 K (or V) bytes.
 __device__ __forceinline__ int chunk8(int s, int c) { return s * D + ((c ^ (s & 7)) << 4); }
 

@@ -232,8 +232,12 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
       uint8_t* const t = ring + n % D8_NB * TILE8_BYTES;
       if ((have >> (j % D8_NB)) & 1) {
         const int first = (tile0 + warp + D8_WARPS * j) * TILE_TOKENS;
-        if (x.ctx - first < TILE_TOKENS) clear_v_rows8(t, x.ctx - first);
-        tile8<CODE, FEW>(t, seen - first, qa, qs, r);
+        if (written8(*reinterpret_cast<const float2*>(t + TILE8_SCALES))) {
+          if (x.ctx - first < TILE_TOKENS) clear_v_rows8(t, x.ctx - first);
+          tile8<CODE, FEW>(t, seen - first, qa, qs, r);
+        } else if (lane == 0 && a.v.status) {
+          atomicOr(a.v.status, IQ_DEVERR_PAGE);
+        }
       }
       __syncwarp();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // this slot's reads before the next copy into it

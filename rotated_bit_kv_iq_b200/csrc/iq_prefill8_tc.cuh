@@ -504,11 +504,11 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
           if (page >= 0 && page < a.v.n_pages) {
             rec = (page * Hkv + s.kvh) * page_tiles + at % page_tiles;
             sc = *reinterpret_cast<const float2*>(a.v.pool + (size_t)rec * TILE8_BYTES + TILE8_SCALES);
-          } else if (a.v.status) {
-            atomicOr(a.v.status, IQ_DEVERR_PAGE);
+            if (!written8(sc)) rec = -1;  // nor are its codes read: they may be NaN
           }
+          if (rec < 0 && a.v.status) atomicOr(a.v.status, IQ_DEVERR_PAGE);
         }
-        const bool there = rec >= 0 && sc.y > 0.f;  // (a scale that is no positive number: nothing was written)
+        const bool there = rec >= 0;
         // log2 in two parts: exact for a power of two
         const float lv = there ? (float)((int)(__float_as_uint(sc.y) >> 23) - 127) +
                                      log2f(__uint_as_float((__float_as_uint(sc.y) & 0x7FFFFFu) | 0x3F800000u))

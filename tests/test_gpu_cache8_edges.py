@@ -52,3 +52,53 @@ def test_append_infinities_beside_the_largest_numbers(code, dtype):
         np.testing.assert_array_equal(_codes(h, side, 0, 0, 70), h.o.codes[side, 0, 0, :70])
     assert h.c.status.item() == 0
     h.pool.check("pool")
+
+
+SCALES = [float("nan"), 0.0, -1.0, float("inf"), float("-inf"), -0.0]
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("side", [0, 1])
+def test_records_in_which_nothing_was_written_are_left_out(code, dtype, side):
+    """A K or V scale that is no positive finite number: the record's tokens are left out and flagged, by decode and by
+    prefill, whatever its codes are (here NaN ones too)."""
+    lens = [300, 70, 33, 400]
+    h = _filled(4, 2, 32, 13, code, lens, 70, dtype)
+    bad = {0: [0, 1, 2, 3, 6, 9], 1: [0, 1, 2], 2: [1], 3: []}
+    n = 0
+    for b, tiles in bad.items():
+        for t in tiles:
+            rec = h.c.tiles()[1, int(h.table[b, t])]
+            rec[:, 0, 4096 * (n % 2): 4096 * (n % 2) + 4096] = 0x7F
+            at = 8192 + 4 * side
+            rec[:, 0, at: at + 4] = torch.tensor([SCALES[n % len(SCALES)]]).view(torch.uint8).to(DEV)
+            n += 1
+
+    def keep(b, n):
+        return np.array([p for p in range(n) if p // 32 not in bad[b]], dtype=int)
+
+    def rows(b, n):
+        kv = [h.kv(b, i, n) for i in range(2)]
+        at = keep(b, n)
+        return np.stack([x[0][at] for x in kv]), np.stack([x[1][at] for x in kv])
+
+    q = torch.randn((4, 8, 128), generator=torch.Generator().manual_seed(2)).to(dtype)
+    o = _decode(h, q, lens, 416)
+    assert h.c.status.item() == B.IQ_DEVERR_PAGE and not o[1].any()
+    for b, n in enumerate(lens):
+        _check_rows(o[b], q[b].double().numpy(), *rows(b, n), 128 ** -0.5, dtype)
+    h.c.status.zero_()
+    start, cnt = [260, 30, 0, 360], [40, 40, 33, 40]
+    q = torch.randn((4, 40, 8, 128), generator=torch.Generator().manual_seed(3)).to(dtype)
+    o = _prefill(h, q, start, 416, cnt)
+    assert h.c.status.item() == B.IQ_DEVERR_PAGE
+    for b, s in enumerate(start):
+        assert (o[b, cnt[b]:] == 7.0).all()
+        for i in range(0, cnt[b], 3):
+            _check_rows(o[b, i], q[b, i].double().numpy(), *rows(b, s + i + 1), 128 ** -0.5, dtype, one_term=dtype != F32)
+    # behind the last token a record may hold anything
+    h.c.status.zero_()
+    assert not _decode(h, q[:, 0], [0, 0, 0, 0], 416).any()
+    _decode(h, q[:, 0], [0, 0, 32, 0], 416)
+    assert h.c.status.item() == 0
