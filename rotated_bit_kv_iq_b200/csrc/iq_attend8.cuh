@@ -58,9 +58,9 @@ __device__ __forceinline__ float load_q8(const void* q, int dtype, size_t row, b
   }
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // exponent of amax clamped so that both powers below are normal numbers
+  // exponent of amax clamped, for zeros and infinities, so that both powers below are normal numbers
   int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-  ex = max(-100, min(126, ex));
+  ex = max(-100, min(127, ex));
   const float sig = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

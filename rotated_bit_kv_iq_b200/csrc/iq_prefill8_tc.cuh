@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
                                    fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
         }
         int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-        ex = max(-100, min(126, ex));
+        ex = max(-100, min(127, ex));
         const float sig = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
         if (live) qs = a.scale * kLog2E8 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
 #pragma unroll

@@ -102,3 +102,29 @@ def test_records_in_which_nothing_was_written_are_left_out(code, dtype, side):
     assert not _decode(h, q[:, 0], [0, 0, 0, 0], 416).any()
     _decode(h, q[:, 0], [0, 0, 32, 0], 416)
     assert h.c.status.item() == 0
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_queries_near_the_largest_number(code, dtype):
+    """Finite queries up to the type's largest number over keys so small that the scores are ordinary."""
+    big = torch.finfo(dtype).max
+    h = Held(2, 1, 64, 2, code)
+    k = torch.zeros((2, 100, 1, 128))
+    k[..., :3] = torch.randint(-8, 9, (2, 100, 1, 3), generator=torch.Generator().manual_seed(1)) * 2.0 ** -100
+    v = _tokens(2, (2, 100, 1, 128), dtype)
+    h.append(k.to(dtype), v, [0, 0])
+    q = torch.zeros((2, 4, 128))
+    q[:, 0, 0] = big
+    q[:, 1, :2] = torch.tensor([2.0 ** 127, -big])
+    q[:, 2, :3] = torch.tensor([-big, 2.0 ** 126, 1.0])
+    q[:, 3, :2] = torch.tensor([big / 2, big])
+    q = q.to(dtype)
+    o = _decode(h, q, [100, 37], 128, 2.0 ** -30)
+    for b, n in enumerate((100, 37)):
+        kk, vv = h.kv(b, 0, n)
+        _check_rows(o[b], q[b].double().numpy(), kk[None], vv[None], 2.0 ** -30, dtype)
+    qq = q[:, None].repeat(1, 9, 1, 1)
+    o = _prefill(h, qq, [91, 20], 128, None, 2.0 ** -30)
+    _check_prefill(h, qq, o, [91, 20], [9, 9], dtype, 2.0 ** -30)
+    assert h.c.status.item() == 0
