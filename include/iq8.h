@@ -215,7 +215,8 @@ iq_status iq_pages_fork(const iq_pages* pages, const iq_page_pool* pools_host, i
                         size_t workspace_bytes, iq_stream_t stream);
 
 /* Moves the held pages to the front of the pools: with N pages held, the k-th held page at or above N moves
- * to the k-th free one below N; tables and counts follow.  n_held_dev (or NULL) gets N. */
+ * to the k-th free one below N; tables and counts follow.  n_held_dev (or NULL) gets N.  An entry that names a page
+ * that nobody holds, or none of the pool's, stays as it is (IQ_DEVERR_PAGE). */
 iq_status iq_pages_compact(const iq_pages* pages, const iq_page_pool* pools_host, int32_t n_pools,
                            int32_t* n_held_dev, void* workspace_dev, size_t workspace_bytes, iq_stream_t stream);
 

@@ -79,6 +79,8 @@ class Pages:
         holes = [p for p in range(held) if self.ref[p] <= 0]
         movers = [p for p in range(held, len(self.ref)) if self.ref[p] > 0]
         to = dict(zip(movers, holes))
+        if any(p >= len(self.ref) or (p >= 0 and self.ref[p] <= 0) for r in self.table for p in r):
+            self.status |= PAGE  # entries of pages that nobody holds, which stay as they are
         for s, d in to.items():
             for pool in self.pools:
                 pool[:, d] = pool[:, s]

@@ -15,13 +15,13 @@ constexpr int PG_THREADS = 1024;
 constexpr int PG_WARPS = PG_THREADS / 32;
 constexpr int PG_PER = IQ_PAGES_MAX_LIST / PG_THREADS;  // list entries per thread
 
-// Workspace: [0] entries to copy, [1] pages held; then the lists.
+// Workspace: the number of entries to copy; then the lists.
 struct PagesWs {
   int32_t* count;
   int32_t* src;    // page copied from
   int32_t* dst;    // page copied to
   int32_t* tiles;  // tile records of each head to copy
-  int32_t* remap;  // per page: where it went (compact), or the free pages in order (extend, fork)
+  int32_t* remap;  // per page: where it is now, -1 if nobody holds it (compact), or the free pages in order (extend, fork)
 };
 static size_t list_len(const iq_pages& p) { return std::max((size_t)IQ_PAGES_MAX_LIST, (size_t)p.n_pages); }
 size_t pages_workspace_bytes(const iq_pages& p) { return 256 + sizeof(int32_t) * (3 * list_len(p) + p.n_pages); }
@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(iq_pages p, i
   pdl_wait();
   __shared__ int scratch[PG_WARPS + 1];
   int32_t* const ref = p.ref_dev;
+  for (int g = threadIdx.x; g < p.n_pages; g += PG_THREADS) w.remap[g] = ref[g] > 0 ? g : -1;
   const int held = rank_pages(p.n_pages, scratch, [&](int g) { return ref[g] > 0; }, [](int, int) {});
   __syncthreads();
   const int holes = rank_pages(p.n_pages, scratch, [&](int g) { return g < held && ref[g] <= 0; },
@@ -288,20 +289,20 @@ __global__ void __launch_bounds__(PG_THREADS) pages_compact_kernel(iq_pages p, i
   }
   if (threadIdx.x == 0) {
     w.count[0] = holes;
-    w.count[1] = held;
     if (n_held) *n_held = held;
   }
 }
 
-// The tables after a compaction: an entry at or above the number of held pages has moved.
+// The tables after a compaction.  An entry of a page that nobody holds stays as it is.
 __global__ void __launch_bounds__(256) pages_remap_kernel(iq_pages p, PagesWs w) {
   pdl_wait();
   const size_t n = (size_t)p.max_seqs * p.max_pages_per_seq;
-  const int held = w.count[1];
-  if (w.count[0] == 0) return;
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
     const int g = p.block_table_dev[i];
-    if (g >= held && g < p.n_pages) p.block_table_dev[i] = w.remap[g];
+    if (g < 0) continue;
+    const int to = g < p.n_pages ? w.remap[g] : -1;
+    if (to < 0) flag(p, IQ_DEVERR_PAGE);
+    else if (to != g) p.block_table_dev[i] = to;
   }
 }
 
