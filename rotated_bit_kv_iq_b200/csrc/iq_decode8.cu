@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   __shared__ __align__(8) uint64_t bars[D8_WARPS][D8_NB];
   __shared__ float sml[D8_WARPS][A8_ROWS][4];
   __shared__ long long s_scan[D8_WARPS];
-  __shared__ int s_most[D8_WARPS];
+  __shared__ int s_most[D8_WARPS], s_live[D8_WARPS];
   __shared__ int s_start[2];  // the CTA's first entry, and the cost before it within all kv heads
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
@@ -102,36 +102,50 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   // ---- plan: total cost, this CTA's range, the sequence that it starts in.  A group is D8_LEAD places and its tiles.
   const int E = a.batch * a.n_blk, per = (E + D8_THREADS - 1) / D8_THREADS, e0 = min(E, tid * per), e1 = min(E, e0 + per);
   long long mine = 0;
-  int most = 0;  // tiles of an entry
+  int most = 0, live = 0;  // tiles of an entry; entries that have any
   for (int e = e0; e < e1; ++e) {
     const int n = d8_tiles<CHUNK>(a, e);
     mine += d8_cost(n);
     most = max(most, n);
+    live += n > 0;
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) s_most[warp] = most;
   long long incl = mine;
+  int incl_live = live;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    const int y = __shfl_up_sync(0xffffffffu, incl_live, o);
+    if (lane >= o) {
+      incl += x;
+      incl_live += y;
+    }
   }
-  if (lane == 31) s_scan[warp] = incl;
+  if (lane == 31) {
+    s_most[warp] = most;
+    s_scan[warp] = incl;
+    s_live[warp] = incl_live;
+  }
   __syncthreads();
-  long long before = incl - mine, total = 0;
+  for (int w = 0; w < D8_WARPS; ++w) most = max(most, s_most[w]);
+  // Short groups, of two rounds of the warps at the most, are not cut: each counts one, and there is nothing to merge (a
+  // 512-token layer of two kv heads: 9 us a call, 15 cut).
+  const bool uncut = most <= D8_UNCUT;
+  auto cost = [&](int tiles) { return uncut ? (tiles > 0 ? 1 : 0) : d8_cost(tiles); };
+  long long before = uncut ? incl_live - live : incl - mine, total = 0;
   for (int w = 0; w < D8_WARPS; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-    most = max(most, s_most[w]);
+    const long long x = uncut ? s_live[w] : s_scan[w];
+    if (w < warp) before += x;
+    total += x;
   }
   before *= Hkv;
   total *= Hkv;
-  // the CTAs that share the tiles: none without one, and no more than give every warp one
-  const int N = (int)min((long long)gridDim.x, max(1ll, (total + D8_WARPS - 1) / D8_WARPS));
+  // the CTAs that share the work: none without a tile, and no more than give every warp one
+  const int N = (int)min((long long)gridDim.x, max(1ll, uncut ? total : (total + D8_WARPS - 1) / D8_WARPS));
   const long long lo = c < N ? c * total / N : total, hi = c < N ? (c + 1) * total / N : total;
   long long acc = before;  // cost of all groups before entry e
   for (int e = e0; e < e1 && acc <= lo; ++e) {
-    const long long n = (long long)Hkv * d8_cost(d8_tiles<CHUNK>(a, e));
+    const long long n = (long long)Hkv * cost(d8_tiles<CHUNK>(a, e));
     if (lo < hi && lo < acc + n) {
       s_start[0] = e;
       s_start[1] = (int)(lo - acc);
@@ -156,34 +170,13 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
         for (int i = tid; i < a.n_q_heads * (D / 4); i += D8_THREADS)
           store4(a.out, a.dtype, (size_t)b * a.n_q_heads * D + 4 * i, make_float4(0.f, 0.f, 0.f, 0.f));
   __syncthreads();
-  // Short groups, of two rounds of the warps at the most, are not cut: CTA c takes groups c, c + grid, ... whole, and there
-  // is nothing to merge (a 512-token layer of two kv heads: 9 us a call, 15 cut).
-  const bool uncut = most <= D8_UNCUT;
-  if (!uncut && lo >= hi) return;
-  int e = 0, kvh = 0, nt = 0, at = 0;  // nt: the group's tiles; at: where in the group's places the segment starts
-  D8Entry x = {};
-  long long pos = lo, gi = c;
-  auto take = [&]() {  // uncut: the next group that has tiles, from gi on; whether there is one
-    for (; gi < (long long)E * Hkv; gi += gridDim.x) {
-      e = (int)(gi / Hkv);
-      kvh = (int)(gi % Hkv);
-      x = d8_entry<CHUNK>(a, e);
-      nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
-      if (nt) return true;
-    }
-    return false;
-  };
-  bool more;
-  if (uncut) {
-    more = take();
-  } else {
-    e = s_start[0];
-    x = d8_entry<CHUNK>(a, e);
-    nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;
-    kvh = s_start[1] / d8_cost(nt);
-    at = s_start[1] % d8_cost(nt);
-    more = true;
-  }
+  if (lo >= hi) return;
+  int e = s_start[0];
+  D8Entry x = d8_entry<CHUNK>(a, e);
+  int nt = (x.ctx + TILE_TOKENS - 1) / TILE_TOKENS;                       // the group's tiles
+  int kvh = s_start[1] / cost(nt), at = s_start[1] % cost(nt);            // at: where in the group's places the segment starts
+  long long pos = lo;
+  bool more = true;
   uint32_t used = 0;  // of this warp's ring, so far
   bool ok = true;
   uint8_t* const ring = smem + warp * D8_NB * TILE8_BYTES;
@@ -194,8 +187,8 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
   };
   while (more) {
     // ---- one segment: tiles [tile0, tile1) of group (e, kvh)
-    const int end = uncut ? d8_cost(nt) : (int)min((long long)d8_cost(nt), at + (hi - pos));
-    const int tile0 = max(0, at - D8_LEAD), tile1 = end - D8_LEAD;
+    const int end = (int)min((long long)cost(nt), at + (hi - pos));
+    const int tile0 = uncut ? 0 : max(0, at - D8_LEAD), tile1 = uncut ? nt : end - D8_LEAD;
     if (tile1 <= tile0) break;  // the range ends before the group's first tile
     const int mine = ok && tile1 - tile0 > warp ? (tile1 - tile0 - warp + D8_WARPS - 1) / D8_WARPS : 0;  // this warp's
     auto issue = [&](int j) {  // the warp's j-th tile of the segment; whether it has a page
@@ -344,11 +337,6 @@ __global__ void __launch_bounds__(D8_THREADS, 1) decode8_kernel(Decode8Args a) {
     // sml, s_last and the sums are read before the next segment's copies and sums take their place
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    if (uncut) {
-      gi += gridDim.x;
-      more = take();
-      continue;
-    }
     pos += end - at;
     at = 0;
     more = pos < hi;

@@ -128,3 +128,23 @@ def test_queries_near_the_largest_number(code, dtype):
     o = _prefill(h, qq, [91, 20], 128, None, 2.0 ** -30)
     _check_prefill(h, qq, o, [91, 20], [9, 9], dtype, 2.0 ** -30)
     assert h.c.status.item() == 0
+
+
+@pytest.mark.parametrize("live", [1.0, 0.15])
+@pytest.mark.parametrize("G,hkv", [(6, 2), (1, 3), (8, 1)])
+def test_float32_chunks_of_many_short_sequences(live, G, hkv):
+    """More blocks than CTAs, none of them cut, many without a token: every live one is computed, once."""
+    r = np.random.default_rng(7)
+    batch, n = 60, 19
+    cnt = [int(r.integers(1, n + 1)) if r.random() < live else 0 for _ in range(batch)]
+    start = [int(r.integers(0, 130)) for _ in range(batch)]
+    h = _filled(batch, hkv, 32, 5, "s8", [s + c for s, c in zip(start, cnt)], 80, F32)
+    q = torch.randn((batch, n, G * hkv, 128), generator=torch.Generator().manual_seed(4))
+    o = _prefill(h, q, start, 160, cnt)
+    _check_prefill(h, q, o, start, cnt, F32, stride=4)
+    assert h.c.status.item() == 0
+    lens = [s if c else 0 for s, c in zip(start, cnt)]  # and decode, sequences of no tokens among them
+    o = _decode(h, q[:, 0], lens, 160)
+    for b, m in enumerate(lens):
+        kv = [h.kv(b, i, m) for i in range(hkv)]
+        _check_rows(o[b], q[b, 0].double().numpy(), np.stack([x[0] for x in kv]), np.stack([x[1] for x in kv]), 128 ** -0.5, F32)
