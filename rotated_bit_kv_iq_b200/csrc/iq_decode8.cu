@@ -22,7 +22,10 @@ constexpr int D8_NB = 2;                                       // tile records i
 constexpr int D8_UNCUT = 2 * D8_WARPS;                         // tiles of a group that is not cut
 // What a group costs beside its tiles (its queries, an empty ring, the warps' merge), in tiles, about 6 us: without it the
 // CTAs that get many short groups are the last (the 16-sequence layer: CTAs of 63 to 90 us; with it 62 to 80).  Leads of
-// 0, 8, 16, 24, 32, 48, 64: 96, 90, 88, 84, 82, 83, 84 us.
+// 0, 8, 16, 24, 32, 48, 64: 96, 90, 88, 84, 82, 83, 84 us.  Other shapes, cold caches, leads of 0 / 16 / 32, us a call with
+// its events: 128 sequences of 100 to 4096 tokens, 8 kv heads 180 / 136 / 127; 64 of 2048 74 / 73 / 74; 4 of 8192 35 / 33 / 31;
+// one of 131072 76 / 73 / 71, of 32768 36 / 33 / 31, of 4096 22.5 / 18.4 / 18.4.  A lead longer than a CTA's share leaves some CTAs
+// of a small call without a tile, but has a group cut into fewer pieces to merge: held to half of the share, 22.5 for 4096 tokens.
 constexpr int D8_LEAD = 32;
 constexpr int D8_SMEM = D8_WARPS * D8_NB * TILE8_BYTES;        // (at a segment's end: the warps' value sums)
 static_assert(D8_WARPS * A8_ROWS * D * 4 <= D8_SMEM, "value sums in the rings' place");
@@ -376,11 +379,10 @@ static int launch8(Decode8Args& a, int n_q_heads, float scale, const void* q, in
   a.part_ml = (float4*)workspace;
   a.part_o = (float*)(a.part_ml + part8_slots() * A8_ROWS);
   a.counters = (int32_t*)((uint8_t*)workspace + part8_bytes());
-  const bool few = a.g_real * a.tq <= 4, e4 = a.v.code == IQ_E4M3;
-  auto fn = a.ctx_len ? (few ? (e4 ? decode8_kernel<IQ_E4M3, true, false> : decode8_kernel<IQ_S8, true, false>)
-                             : (e4 ? decode8_kernel<IQ_E4M3, false, false> : decode8_kernel<IQ_S8, false, false>))
-                      : (few ? (e4 ? decode8_kernel<IQ_E4M3, true, true> : decode8_kernel<IQ_S8, true, true>)
-                             : (e4 ? decode8_kernel<IQ_E4M3, false, true> : decode8_kernel<IQ_S8, false, true>));
+  const bool few = a.g_real <= 4, e4 = a.v.code == IQ_E4M3;  // (a chunk's blocks have five rows or more)
+  auto fn = !a.ctx_len ? (e4 ? decode8_kernel<IQ_E4M3, false, true> : decode8_kernel<IQ_S8, false, true>)
+            : few      ? (e4 ? decode8_kernel<IQ_E4M3, true, false> : decode8_kernel<IQ_S8, true, false>)
+                       : (e4 ? decode8_kernel<IQ_E4M3, false, false> : decode8_kernel<IQ_S8, false, false>);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, D8_SMEM);
   if (e != cudaSuccess) return (int)e;
   return (int)launch_pdl(fn, dim3(n), dim3(D8_THREADS), D8_SMEM, (cudaStream_t)stream, a);
