@@ -8,7 +8,7 @@ import torch
 
 from oracle import cache8
 from rotated_bit_kv_iq_b200 import binding as B
-from tests.test_gpu_cache8 import BF16, DEV, F16, F32, Held, _check_prefill, _check_rows, _decode, _filled, _i32, _prefill, _tokens  # noqa: F401
+from tests.test_gpu_cache8 import BF16, DEV, F16, F32, Held, _check_prefill, _check_rows, _decode, _filled, _i32, _prefill, _tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -127,6 +127,43 @@ def test_queries_near_the_largest_number(code, dtype):
     qq = q[:, None].repeat(1, 9, 1, 1)
     o = _prefill(h, qq, [91, 20], 128, None, 2.0 ** -30)
     _check_prefill(h, qq, o, [91, 20], [9, 9], dtype, 2.0 ** -30)
+    assert h.c.status.item() == 0
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("small", [0, 2, 6])
+def test_decode_small_values_beside_large_ones(code, dtype, small):
+    """The block `small` of V's of 2^-12 (2^-30 in float32) has all the weight, the others, of V's of 2^12 (2^30), none: what
+    comes out is the small block's, to the tolerance of the block's own values.  Per value, with w the weights and m_i =
+    w_i times the largest |V| of i's block: sum w |V| (1.5 e_s + 2^-20 + T 2^-24), and, since weights times block scales are
+    held in two binary16 terms of steps down to 2^-24 below their maximum (a code times scale at most twice the largest
+    |V| of the block), T 2^-24 max m_i; and half a step of the output's type."""
+    e, T, scale = (30, 224, 0.1) if dtype == F32 else (10, 224, 0.1)
+    h = Held(1, 1, 256, 1, code, contiguous=True)
+    k, v = 0.2 * _tokens(60, (1, T, 1, 128), F32), _tokens(61, (1, T, 1, 128), F32)
+    q = torch.randn((1, 4, 128), generator=torch.Generator().manual_seed(3)).to(dtype)
+    q[..., 9] = 30.0
+    lo, hi = 32 * small, 32 * small + 32
+    k[..., 9] = -60.0  # score 30 * -60 * 0.1 = -180: weight 2^-260
+    k[:, lo:hi, :, 9] = 0.0
+    v *= 2.0 ** e
+    v[:, lo:hi] *= 2.0 ** (-2 * e)
+    h.append(k, v, [0])
+    kk, vv = h.kv(0, 0, T)
+    o = _decode(h, q, [T], 256, scale)[0]
+    x = q[0].double().numpy()
+    s = scale * x @ kk.T
+    w = np.exp(s - s.max(axis=1, keepdims=True))
+    w /= w.sum(axis=1, keepdims=True)
+    want = w @ vv
+    assert np.abs(want).max() < 2.0 ** (6 - e)  # the large blocks have no part in it
+    es = np.log2(np.e) * scale * (np.abs(x) @ np.abs(kk).T).max() * (2.0 ** -22 + 132 * 2.0 ** -24)
+    top = np.abs(vv).reshape(-1, 32 * 128).max(axis=1).repeat(32)
+    tol = w @ np.abs(vv) * (1.5 * es + 2.0 ** -20 + T * 2.0 ** -24) + T * 2.0 ** -24 * (w * top).max(axis=1, keepdims=True)
+    half = {F32: 2.0 ** -24, F16: 2.0 ** -11}[dtype]
+    tol += np.abs(want) * half + (2.0 ** -25 if dtype == F16 else 0.0)
+    assert (np.abs(o - want) <= tol).all(), (np.abs(o - want) / tol).max()
     assert h.c.status.item() == 0
 
 
