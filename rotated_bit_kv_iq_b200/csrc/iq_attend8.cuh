@@ -18,6 +18,9 @@ namespace iq {
 
 constexpr int A8_ROWS = 8;  // query rows of a warp (the group's heads)
 constexpr float kLog2E8 = 1.4426950408889634f;
+// log2 of what probabilities are held times in binary16: the largest is below 2^15 then, and weights 2^-17 of it still have
+// 22 bits in their two terms, whose steps of 2^-24 are 2^-38 of it.
+constexpr float A8_ABOVE = 14.f;
 
 __device__ __forceinline__ void hmma8(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -31,7 +34,7 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
 __device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
 // Running softmax of row g (in log2 units) and the warp's value sums.  The values' block scales are
-// folded into the probabilities: sums are of p * vs / 2^(mo - m), with a running maximum mo of (score +
+// folded into the probabilities: sums are of p * vs * 2^14 / 2^(mo - m), with a running maximum mo of (score +
 // log2 of the block's scale) of its own, so that neither the scores' nor the scales' range matters.
 struct Row8 {
   float m, mo, l;  // running maxima; this lane's share of the sum
@@ -127,8 +130,8 @@ __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32
     r.m = m;
     r.mo = mo;
   }
-  // p * vs / 2^(mo - m), at most 2
-  const float fac = mo == -CUDART_INF_F ? 0.f : fast_exp2(fminf(m + vexp - mo, 126.f)) * vman;
+  // p * vs * 2^14 / 2^(mo - m), below 2^15
+  const float fac = mo == -CUDART_INF_F ? 0.f : fast_exp2(fminf(m + vexp - mo + A8_ABOVE, 126.f)) * vman;
   uint32_t ph[4], pl[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {

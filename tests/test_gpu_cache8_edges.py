@@ -185,3 +185,55 @@ def test_float32_chunks_of_many_short_sequences(live, G, hkv):
     for b, m in enumerate(lens):
         kv = [h.kv(b, i, m) for i in range(hkv)]
         _check_rows(o[b], q[b, 0].double().numpy(), np.stack([x[0] for x in kv]), np.stack([x[1] for x in kv]), 128 ** -0.5, F32)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("down", [20.3, 24.6, 26.2, 31.0])
+@pytest.mark.parametrize("batch,T", [(1, 700), (40, 700), (1, 3000), (300, 1500)])
+def test_keys_far_below_the_first(code, dtype, down, batch, T):
+    """Behind a first key with nearly all the weight and V = 0, keys of 2^-down of it that have all of V: decode, and a chunk
+    of float32.  Weights times block scales are held in two binary16 terms of steps down to 2^-24, their maximum being 2^14
+    or more: a key is off by 2^-39 of that, and a code times scale is at most twice the largest |V|: T 2^-38 in all, beside
+    sum w |V| (1.5 e_s + 2^-20 + T 2^-24) and half a step of the output's type."""
+    hkv, G = 2, 4
+    per = -(-T // 64)
+    c = B.PagedCache8(1, hkv, 64, per, code=code, block_table=torch.arange(per, dtype=torch.int32, device=DEV).repeat(batch, 1))
+    k, v = torch.zeros((1, T, hkv, 128), device=DEV), torch.ones((1, T, hkv, 128), device=DEV)
+    k[:, 0, :, 7] = 240.0
+    v[:, 0] = 0.0
+    one = B.PagedCache8(1, hkv, 64, per, code=code, block_table=c.block_table[:1].contiguous(), pool=c.pool)
+    B.iq_append8(one, 0, k, v, _i32([0]))  # every sequence reads the same pages
+    kv = []
+    for side in (0, 1):
+        x = torch.empty((hkv, T, 128), dtype=F32, device=DEV)
+        B.iq_export8(one, 0, side, 0, 0, T, x)
+        kv.append(x[0].double().cpu().numpy())
+    scale = down * float(np.log(2.0)) / kv[0][0, 7]
+    scale = float(np.float32(scale))
+    s = scale * kv[0][:, 7]
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    q = torch.zeros((batch, hkv * G, 128), dtype=dtype, device=DEV)
+    q[..., 7] = 1.0
+    es = np.log2(np.e) * s.max() * (2.0 ** -22 + 132 * 2.0 ** -24)
+
+    def check(o, w, n):
+        want = float(w @ kv[1][:n, 0])
+        tol = want * (1.5 * es + 2.0 ** -20 + n * 2.0 ** -24) + n * 2.0 ** -38 + want * (2.0 ** -11 if dtype == F16 else 2.0 ** -24)
+        tol += 2.0 ** -25 if dtype == F16 else 0.0
+        assert np.abs(o - want).max() <= tol, (np.abs(o - want).max() / tol, o.min(), o.max(), want)
+
+    out = torch.full_like(q, float("nan"))
+    ws = torch.zeros(B.iq_decode8_workspace_size(batch, hkv * G, hkv, per * 64), dtype=torch.uint8, device=DEV)
+    B.iq_decode8_attention(c, 0, q, _i32([T] * batch), per * 64, out, ws, scale)
+    check(out.double().cpu().numpy(), w, T)
+    if dtype == F32:
+        q = q[:, None].repeat(1, 3, 1, 1)
+        out = torch.full_like(q, float("nan"))
+        ws = torch.zeros(B.iq_prefill8_workspace_size(batch, 3, hkv * G, hkv, per * 64), dtype=torch.uint8, device=DEV)
+        B.iq_prefill8_attention(c, 0, q, _i32([T - 3] * batch), per * 64, out, ws, scale=scale)
+        for i in range(3):
+            n = T - 2 + i
+            check(out[:, i].double().cpu().numpy(), w[:n] / w[:n].sum(), n)
+    assert c.status.item() == 0
