@@ -18,8 +18,8 @@ namespace iq {
 
 constexpr int A8_ROWS = 8;  // query rows of a warp (the group's heads)
 constexpr float kLog2E8 = 1.4426950408889634f;
-// log2 of what probabilities are held times in binary16: the largest is below 2^15 then, and weights 2^-17 of it still have
-// 22 bits in their two terms, whose steps of 2^-24 are 2^-38 of it.
+// log2 of what probabilities and their sums are held times: times V's scale, in binary16, the largest is below 2^15 then, and
+// weights 2^-17 of it still have 22 bits in their two terms, whose steps of 2^-24 are 2^-38 of it.
 constexpr float A8_ABOVE = 14.f;
 
 __device__ __forceinline__ void hmma8(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -34,10 +34,10 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
 __device__ __forceinline__ float2 half2_floats(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
 // Running softmax of row g (in log2 units) and the warp's value sums.  The values' block scales are
-// folded into the probabilities: sums are of p * vs * 2^14 / 2^(mo - m), with a running maximum mo of (score +
+// folded into the probabilities: sums are of p * vs / 2^(mo - m), with a running maximum mo of (score +
 // log2 of the block's scale) of its own, so that neither the scores' nor the scales' range matters.
 struct Row8 {
-  float m, mo, l;  // running maxima; this lane's share of the sum
+  float m, mo, l;  // running maxima; this lane's share of the sum, times 2^14 as o is
   float o[8][4];   // o[i]: coordinates 16 g + 2 i (entries 0, 1) and + 1 (2, 3) of rows 2 t and 2 t + 1
 };
 __device__ __forceinline__ void row8_init(Row8& r) {
@@ -130,13 +130,13 @@ __device__ __forceinline__ void tile8(const uint8_t* tile, int lim, const uint32
     r.m = m;
     r.mo = mo;
   }
-  // p * vs * 2^14 / 2^(mo - m), below 2^15
-  const float fac = mo == -CUDART_INF_F ? 0.f : fast_exp2(fminf(m + vexp - mo + A8_ABOVE, 126.f)) * vman;
+  // p * vs / 2^(mo - m), below 2^15
+  const float fac = mo == -CUDART_INF_F ? 0.f : fast_exp2(fminf(m + vexp - mo, 126.f)) * vman, at = m - A8_ABOVE;
   uint32_t ph[4], pl[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const float p0 = s[2 * n] == -CUDART_INF_F ? 0.f : fast_exp2(s[2 * n] - m);
-    const float p1 = s[2 * n + 1] == -CUDART_INF_F ? 0.f : fast_exp2(s[2 * n + 1] - m);
+    const float p0 = s[2 * n] == -CUDART_INF_F ? 0.f : fast_exp2(s[2 * n] - at);
+    const float p1 = s[2 * n + 1] == -CUDART_INF_F ? 0.f : fast_exp2(s[2 * n + 1] - at);
     r.l += p0 + p1;
     const float x0 = p0 * fac, x1 = p1 * fac;
     ph[n] = half2_bits(x0, x1);

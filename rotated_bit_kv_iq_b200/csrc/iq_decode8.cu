@@ -79,7 +79,7 @@ __device__ __forceinline__ int d8_cost(int tiles) { return tiles ? tiles + D8_LE
 
 // Final value of one row of the group: lane holds sums of coordinates 4 lane ..
 __device__ __forceinline__ void finish_row8(const Decode8Args& a, size_t row, float M, float MO, float L, float4 o) {
-  const float f = L > 0.f ? fast_exp2(MO - M - A8_ABOVE) / L : (L == L ? 0.f : L);
+  const float f = L > 0.f ? fast_exp2(MO - M) / L : (L == L ? 0.f : L);
   store4(a.out, a.dtype, row * D + 4 * (threadIdx.x & 31), make_float4(o.x * f, o.y * f, o.z * f, o.w * f));
 }
 

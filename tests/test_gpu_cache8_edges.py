@@ -237,3 +237,30 @@ def test_keys_far_below_the_first(code, dtype, down, batch, T):
             n = T - 2 + i
             check(out[:, i].double().cpu().numpy(), w[:n] / w[:n].sum(), n)
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("apart", [100, 116, 122])
+def test_decode_small_weights_of_very_large_values(code, apart):
+    """A block whose keys have 2^-apart of the others' weight, and values 2^(apart + 4) times as large: they are what comes
+    out."""
+    T = 96
+    h = Held(1, 1, 96, 1, code, contiguous=True)
+    k, v = torch.zeros((1, T, 1, 128)), _tokens(62, (1, T, 1, 128), F32)
+    k[:, 32:64, :, 9] = -60.0
+    v *= 2.0 ** -64
+    v[:, 32:64] *= 2.0 ** (apart + 4)
+    q = torch.zeros((1, 4, 128))
+    q[..., 9] = 8.0
+    h.append(k, v, [0])
+    kk, vv = h.kv(0, 0, T)
+    scale = float(np.float32(apart * np.log(2.0) / (-kk[32, 9] * 8.0)))
+    o = _decode(h, q, [T], 96, scale)[0]
+    s = scale * q[0].double().numpy() @ kk.T
+    w = np.exp(s - s.max(axis=1, keepdims=True))
+    w /= w.sum(axis=1, keepdims=True)
+    want, mass = w @ vv, w @ np.abs(vv)
+    es = apart * (2.0 ** -22 + 132 * 2.0 ** -24)
+    tol = mass * (1.5 * es + 2.0 ** -20 + T * 2.0 ** -24) + T * 2.0 ** -38 * mass.max() * 32 + np.abs(want) * 2.0 ** -24
+    assert np.abs(want).max() > 2.0 ** -64 and (np.abs(o - want) <= tol).all(), (np.abs(o - want) / tol).max()
+    assert h.c.status.item() == 0
