@@ -51,6 +51,9 @@ constexpr float PT_TOP = 65504.f;  // the most that p' of a half-step add up to:
 // log2 of the largest p' of a half-step that sets ref (64 of them are below PT_TOP).  The 2048-token chunk takes 295 us so and
 // 290 with 4, which leaves 12 bits until the next rescaling, not 8; but then 131072 keys are off by 2^-12.
 constexpr float PT_ABOVE = 8.f;
+// log2 of the row's sum beside the first V scale: V scales 2^104 apart leave the sum between 2^-112 and, over T keys,
+// 2^98 T, within float32 either way.
+constexpr float PT_BASE = -16.f;
 
 struct PtSmem {
   static constexpr int q = 0;                 // [tile] 128 rows x 128 coordinates
@@ -59,7 +62,7 @@ struct PtSmem {
   static constexpr int ks = 196608;           // float [8][4]: K scales of step n mod 8's records
   static constexpr int lv = ks + 128;         // float [8][4]: log2 of the V scales; NaN: the record is not there
   static constexpr int w = lv + 128;          // float [8][4]: 2^(base - log2 of the V scale)
-  static constexpr int base = w + 128;        // float [8]: the segment's base, log2 of its first V scale
+  static constexpr int base = w + 128;        // float [8]: the segment's base, PT_BASE and log2 of its first V scale
   static constexpr int rec = base + 32;       // int [4][4]: step n mod 4's records in the layer; -1: not there
   static constexpr int keys = rec + 64;       // int [4]: the step's keys up to the block's last; 0: the run's end
   static constexpr int scan = keys + 16;      // int64 [20], then the plan: int [4]
@@ -401,8 +404,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         const float base = reinterpret_cast<const float*>(smem + SM::base)[(n + s.k1 - s.k0 - 1) & 7];
         const float inv = l > 0.f ? fast_exp2(base) / l : (l == l ? 0.f : l);
         const size_t prow = (size_t)(2 * c + (s.pos == 0 ? 0 : 1)) * PT_ROWS + r;
-        if (!whole)
-          a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f) : make_float4(ref - base, ref, l, 0.f);
+        if (!whole) {
+          // the sum as its exponent and a number in [1, 2), since sums of segments of other bases are far from it
+          const int ex = l > 0.f && l < CUDART_INF_F ? ilogbf(l) : 0;
+          a.part_ml[prow] = l == 0.f ? make_float4(-CUDART_INF_F, -CUDART_INF_F, 0.f, 0.f)
+                                     : make_float4(ref - base + (float)ex, ref, ldexpf(l, -ex), 0.f);
+        }
 #pragma unroll 1
         for (int b = 0; b < 8; ++b) {
           uint32_t x[16];
@@ -490,6 +497,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
       // ==== where the records of each step are, and their scales; lane b < 4: record b
       const int page_tiles = a.v.page_size / TILE_TOKENS;
       float base = 0.f, least = CUDART_INF_F, most = -CUDART_INF_F;  // of the segment's log2 of V scales
+      bool based = false;                                            // the segment has had a record
       bool more = true;
       int step = s.k0;
       for (uint32_t n = 0; more; ++n) {
@@ -513,10 +521,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1) prefill8_tc_kernel(PtArgs a) {
         const float lv = there ? (float)((int)(__float_as_uint(sc.y) >> 23) - 127) +
                                      log2f(__uint_as_float((__float_as_uint(sc.y) & 0x7FFFFFu) | 0x3F800000u))
                                : __uint_as_float(0x7FC00000u);
-        if (step == s.k0) {
-          const uint32_t m = __ballot_sync(0xffffffffu, there);
-          const float first = __shfl_sync(0xffffffffu, lv, m ? __ffs(m) - 1 : 0);
-          base = m ? first : 0.f;
+        if (step == s.k0) based = false;
+        if (const uint32_t m = __ballot_sync(0xffffffffu, there); m && !based) {
+          base = __shfl_sync(0xffffffffu, lv, __ffs(m) - 1) + PT_BASE;
+          based = true;
         }
         // p' below 2^-126 is 0, and with it the key's share of the row's sum: of scales within 2^104 of each other (a block
         // of zeros has 2^-100) only keys of weights below 2^-30 are lost so
@@ -695,9 +703,10 @@ static __global__ void __launch_bounds__(32 * PTM_WARPS) prefill8_merge_kernel(P
     for (int j = 0; j < PTM_ROWS; ++j) {
       const int r = r0 + j;
       if (r >= rows) break;
-      const float f = L[j] > 0.f ? fast_exp2(MO[j] - M[j]) / L[j] : (L[j] == L[j] ? 0.f : L[j]);
+      // (of a long context whose V scales are the smallest the factor itself is below float32's numbers)
+      const float f = L[j] > 0.f ? fast_exp2(MO[j] - M[j] + 32.f) / L[j] : (L[j] == L[j] ? 0.f : L[j]), g = 0x1p-32f;
       const size_t row = ((size_t)x.b * a.n_tok + x.tok0 + r / G) * a.n_q_heads + (size_t)kvh * G + r % G;
-      store4(a.out, a.dtype, row * D + 4 * lane, make_float4(o[j].x * f, o[j].y * f, o[j].z * f, o[j].w * f));
+      store4(a.out, a.dtype, row * D + 4 * lane, make_float4(o[j].x * f * g, o[j].y * f * g, o[j].z * f * g, o[j].w * f * g));
     }
   }
 }

@@ -281,3 +281,117 @@ def test_zero_blocks_among_others(dtype, code):
     o = _prefill(c, q, [0], 320)
     _check(c, q, o, [0], [n], rows=300)
     assert c.c.status.item() == 0
+
+
+def _check_local(cache, q, o, pos0, scale, rows, gone=None, b=0):
+    """As _check, with what the rows really meet in the place of vtop: a key is off by 2^-32 of the largest weight times
+    largest |V| of a block."""
+    n = q.shape[1]
+    T = pos0 + n
+    k, v = cache.held(b, T)
+    there = torch.ones(T, dtype=torch.bool, device=DEV) if gone is None else ~gone[:T].to(DEV)
+    k[:, ~there], v[:, ~there] = 0.0, 0.0
+    pad = -T % 32
+    top = torch.nn.functional.pad(v.abs().amax(2), (0, pad)).view(cache.hkv, -1, 32).amax(2).repeat_interleave(32, 1)[:, :T]
+    g = q.shape[2] // cache.hkv
+    k, v, top = (x.repeat_interleave(g, 0) for x in (k, v, top))
+    used = 0.0
+    for i in sorted({0, n - 1, *np.linspace(0, n - 1, rows).astype(int).tolist()}):
+        x = q[b, i].double()
+        see = there & (torch.arange(T, device=DEV) <= pos0 + i)
+        w = torch.softmax((scale * torch.einsum("htd,hd->ht", k, x)).masked_fill(~see, float("-inf")), dim=1)
+        want, mass = torch.einsum("ht,htd->hd", w, v), torch.einsum("ht,htd->hd", w, v.abs())
+        es = np.log2(np.e) * scale * torch.einsum("htd,hd->ht", k.abs(), x.abs()).masked_fill(~see, 0.0).amax(1)[:, None]
+        es = es * (2.0 ** -22 + 132 * 2.0 ** -24)
+        tol = mass * (1.5 * es + 2.0 ** -20 + T * 2.0 ** -24 + 2.0 ** -11) + T * 2.0 ** -32 * (w * top).amax(1)[:, None]
+        tol = tol + want.abs() * HALF_STEP[q.dtype] + (2.0 ** -25 if q.dtype == F16 else 0.0)
+        got = o[b, i].double()
+        assert torch.isfinite(got).all(), i
+        share = ((got - want).abs() / tol.clamp_min(1e-300)).max().item()
+        assert share <= 1.0, (i, share)
+        used = max(used, share)
+    return used
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+@pytest.mark.parametrize("missing", [True, False])
+def test_parts_of_a_row_whose_scales_are_far_apart(code, missing):
+    """One step of 128 keys to a CTA: a part whose first block is zeros and whose others are not; and one whose blocks are
+    zeros but count, behind a block of values whose keys count for little (and, missing, one whose first block is not there).
+    Neither part's share of the row's sum is lost where they are merged."""
+    T, n = 1024, 8
+    c = Cache(1, 1, 32, T // 32, code, seed=3)
+    k, v = 0.02 * _tokens(30, (1, T, 1, 128)), _tokens(31, (1, T, 1, 128))
+    k[..., 9] = 0.0
+    v[:, 128:160] = 0.0
+    v[:, 512:640] = 0.0
+    k[:, 512:544, :, 9] = -600.0
+    v[:, 512:544] = _tokens(32, (1, 32, 1, 128))
+    gone = torch.zeros(T, dtype=torch.bool)
+    if missing:
+        v[:, 640:768] = 0.0
+        gone[640:672] = True
+    c.append(k.to(BF16), v.to(BF16))
+    q = 0.3 * _q(33, (1, n, 4, 128), BF16)
+    q[..., 9] = 1.0
+    keep = c.table.clone()
+    if missing:
+        c.table[0, 20] = -1
+    o = _prefill(c, q, [T - n], T)
+    assert c.c.status.item() == (B.IQ_DEVERR_PAGE if missing else 0)
+    c.table.copy_(keep)
+    _check_local(c, q, o, T - n, 128 ** -0.5, n, gone)
+
+
+def test_first_blocks_missing_and_blocks_of_zeros():
+    """Runs of four steps a CTA: some whose first step has no record and whose others are zeros, some that begin with zeros
+    and end with values.  What the zeros weigh stays in the row's sum."""
+    T, n, hkv = 9600, 8, 8
+    c = Cache(1, hkv, 32, T // 32, "e4m3", seed=4)
+    k, v = 0.1 * _tokens(34, (1, T, hkv, 128)), _tokens(35, (1, T, hkv, 128))
+    v[:, 256:1536], v[:, 3840:7680] = 0.0, 0.0
+    c.append(k.to(BF16), v.to(BF16))
+    lost = torch.rand(T // 128, generator=torch.Generator().manual_seed(5)) < 0.5
+    lost[6:20] = False  # (here the first zeros end)
+    lost = lost.repeat_interleave(4)
+    q = _q(36, (1, n, 2 * hkv, 128), BF16)
+    keep = c.table.clone()
+    c.table[0, lost.to(DEV)] = -1
+    o = _prefill(c, q, [T - n], T)
+    assert c.c.status.item() == B.IQ_DEVERR_PAGE
+    c.table.copy_(keep)
+    _check_local(c, q, o, T - n, 128 ** -0.5, n, lost.repeat_interleave(32))
+
+
+@pytest.mark.parametrize("code", ["e4m3", "s8"])
+def test_sums_of_keys_whose_values_are_2_to_the_103_smaller(code):
+    """A first block of V's 2^103 larger than the rest, whose keys weigh 2^-120 of theirs, in a run of hundreds of steps:
+    the sums, in units of the first block's scale, stay finite."""
+    T = 98304
+    n = 64 * torch.cuda.get_device_properties(0).multi_processor_count
+    c = Cache(1, 1, 128, T // 128, code, seed=6)
+    k, v = torch.zeros((1, T, 1, 128), device=DEV), (1.0 + _q(37, (1, T, 1, 128), F32).abs()) * 2.0 ** -50
+    v[:, :32] *= 2.0 ** 103
+    k[:, :32, :, 7] = -240.0
+    k[:, 64:, :, 8] = 8.0
+    c.append(k.to(BF16), v.to(BF16))
+    top = -c.held(0, 1)[0][0, 0, 7].item()
+    scale = 120 * float(np.log(2.0)) / top
+    q = torch.zeros((1, n, 4, 128), dtype=BF16, device=DEV)
+    q[..., 7] = 1.0
+    q[..., 8] = 0.475  # the later keys 2^1.9 above the first ones: the probabilities of a half-step just below their limit
+    o = _prefill(c, q, [T - n], T, scale=scale)
+    assert c.c.status.item() == 0
+    _check_local(c, q, o, T - n, scale, 24)
+
+
+def test_a_million_keys_of_the_smallest_values():
+    T, n = 1 << 20, 4
+    c = Cache(1, 1, 256, T // 256, "e4m3", seed=7)
+    v = _q(38, (1, T, 1, 128), BF16) * 2.0 ** -97 + 2.0 ** -98
+    c.append(_q(39, (1, T, 1, 128), BF16), v)
+    del v
+    q = 0.1 * _q(40, (1, n, 1, 128), BF16)
+    o = _prefill(c, q, [T - n], T)
+    assert c.c.status.item() == 0 and o.double().abs().max().item() > 0
+    _check_local(c, q, o, T - n, 128 ** -0.5, 2)
