@@ -107,7 +107,8 @@ size_t iq_prefill8_workspace_size(int32_t batch, int32_t n_tokens, int32_t n_q_h
  *                    flagged) are there; the rows of `out` behind them are left as they were.
  *   start_pos      : values outside [0, max_ctx - n_valid[b]] are clamped and flagged.
  * With 16-bit queries the V scales of a sequence's blocks of a kv head are to lie within a factor of 2^104 of
- * each other (a block of zeros has 2^-100); what is farther apart is flagged (IQ_DEVERR_RANGE).
+ * each other (a block of zeros has 2^-100); what is farther apart is flagged (IQ_DEVERR_RANGE).  Their softmax weights are
+ * rounded to binary16 before the product with V, 2^-11 of each; float32 queries keep 22 bits of theirs.
  * Other arguments as for iq_decode8_attention.  At most 2^27 kv heads' tokens (batch Hkv n_tokens), and 2^31
  * steps of 128 keys by the blocks of 256 / G tokens (IQ_ERR_UNSUPPORTED above). */
 iq_status iq_prefill8_attention(const iq_cache8* cache, int32_t layer, const void* q_dev, iq_dtype dtype, int32_t batch,

@@ -8,7 +8,7 @@
 // partial (m, mo, l, O), and the last CTA of a group to arrive merges the group's partials in a fixed order, so that results
 // do not depend on who is last.
 // Bound by memory, 257 B for each (token, kv head).  A layer of 16 sequences of 2K to 32K tokens, 32 query and 8 kv heads:
-// 82-88 us, 84-89% of the copy rate.  (Before groups counted for more than their tiles: 94; 105 with eight warps of 197
+// 82-89 us, 82-89% of the copy rate.  (Before groups counted for more than their tiles: 94; 105 with eight warps of 197
 // registers; 121 with sixteen, whose 128 registers do not hold a tile's work, on one ring of 26 records.)
 #include <algorithm>
 

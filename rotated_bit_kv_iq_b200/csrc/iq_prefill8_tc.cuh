@@ -8,7 +8,7 @@
 //                   the cache: rows of coordinates (N-major operand)
 // Each tile has two S buffers: while the softmax is at one half-step's scores the tensor core adds the P of the half-step
 // before and makes the scores of the one after.  (One buffer of 128 keys a tile: 334 us on the 2048-token
-// chunk, 265 so.)
+// chunk, 265 so.  This and the other variants' times are from before ref had its margin, below, which costs 6 us.)
 // The block scales stay out of both products: a score is S times (K scale of its 32 keys) times a row factor, and the V
 // scale joins the exponent, p' = 2^(s + log2 v - ref); the row's sum takes p' / v.  ref is 8 below the first half-step's
 // maximum of s + log2 v, and follows only once the p' of a half-step add up to more than 65504: O is then rescaled in tensor
@@ -25,9 +25,9 @@
 // Roles: warps 0-3 and 4-7 the softmax of the two tiles (thread = row), 8-11 and 12-15 the expansion of K and of V, 16
 // and 18 issue the two tiles' MMAs, 17 finds the records and their scales.
 //
-// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 265 us back to back, 907 TFLOP/s, 54% of cuBLAS's
-// bf16 rate; 291 with the caches flushed between calls.  Of a
-// step's 4,600 cycles the MMAs take 2,500 (a 64-key score product, fed from shared memory, runs at 64% of the MMA rate: 50
+// Measured (2048 tokens after 6144, 32 query and 8 kv heads, int8): 273 us back to back, 880 TFLOP/s, 53% of cuBLAS's
+// bf16 rate; 297 with the caches flushed between calls.  Of a
+// step's 4,700 cycles the MMAs take 2,500 (a 64-key score product, fed from shared memory, runs at 64% of the MMA rate: 50
 // cycles for 32), the exponentials (MUFU) 2,050, instruction issue 2,100 a scheduler; the rest is latency of the softmax
 // warps, two a scheduler.
 #pragma once
@@ -43,13 +43,13 @@ constexpr int PT_ROWS = 256;  // rows of a block
 constexpr int PT_BN = 128;    // keys of a step
 constexpr int PT_THREADS = 640;
 // registers a thread: softmax (two warpgroups), expansion (two), MMA issue; the block is launched with 5 * 96.  The
-// 2048-token chunk takes 265 us so, 273 with 120 / 80 / 80, 269 with 104 / 88 / 96; the MMA warps spill with 64.
+// 2048-token chunk took 265 us so, 273 with 120 / 80 / 80, 269 with 104 / 88 / 96; the MMA warps spill with 64.
 constexpr int PT_REG_SOFTMAX = 112, PT_REG_EXPAND = 80, PT_REG_MMA = 96;
 static_assert(2 * PT_REG_SOFTMAX + 2 * PT_REG_EXPAND + PT_REG_MMA <= 5 * 96, "the register split");
 constexpr int PT_S_COL = 0, PT_O_COL = 256;  // of tile t: 128 columns from PT_S_COL + 128 t, PT_O_COL + 128 t
 constexpr float PT_TOP = 65504.f;  // the most that p' of a half-step add up to: binary16's largest number
-// log2 of the largest p' of a half-step that sets ref (64 of them are below PT_TOP).  The 2048-token chunk takes 295 us so and
-// 290 with 4, which leaves 12 bits until the next rescaling, not 8; but then 131072 keys are off by 2^-12.
+// log2 of the largest p' of a half-step that sets ref (64 of them are below PT_TOP).  The 2048-token chunk takes 295 us so (cold
+// caches) and 290 with 4, which leaves 12 bits until the next rescaling, not 8; but then 131072 keys are off by 2^-12.
 constexpr float PT_ABOVE = 8.f;
 // log2 of the row's sum beside the first V scale: V scales 2^104 apart leave the sum between 2^-112 and, over T keys,
 // 2^98 T, within float32 either way.

@@ -2,8 +2,9 @@
 //
 // One CTA per token: its threads first start the loads of the token's heads, then find the token's
 // rotary_dim / 2 sines and cosines once for all heads (the angle in turns, reduced to [-1/2, 1/2] in
-// double; sine and cosine of that fraction in float32), then turn what they loaded.  A thread owns whole
-// pairs, so that a call may work in place.  Bound by memory: every value read once and written once.
+// double; sine and cosine of that fraction in float32, whose rounding is at most 2^-26 of a turn, 1e-7 rad:
+// float32 outputs are 1.3 times as far from 64 bits as with float64 sines), then turn what they loaded.  A
+// thread owns whole pairs, so that a call may work in place.  Bound by memory: every value read once and written once.
 // 8192 tokens of 40 heads in 16 bits: 29 us, 91% of the copy rate (48 with the angles before the loads); 16 tokens: 5.6 us,
 // latency.
 #include <algorithm>

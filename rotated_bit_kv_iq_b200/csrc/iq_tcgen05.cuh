@@ -53,7 +53,8 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
 
 // Eight MMAs over K = 128 from operands in the layouts above, R = 128 rows (of which B may take a part): the
 // descriptors of the first one, and for the rest the constant steps of their start addresses (in 16-byte units), so
-// that one thread issues them back to back (72-90 cycles each where it made every descriptor anew, 64 now).  A and B
+// that one thread issues them back to back (72-90 cycles each where it made every descriptor anew, 64 so; 52 for 64 keys
+// from a warp that keeps the descriptors in uniform registers).  A and B
 // along K (two blocks of 64): steps 2, 4, 6, 1024, 1026, ...; D is overwritten.
 __device__ __forceinline__ void umma_f16_k128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
 #define IQ_UMMA_STEP(off) "add.u64 a, %1, " #off ";\n add.u64 b, %2, " #off ";\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n "
